@@ -14,6 +14,7 @@
 
 #include "mk_isa.h"
 #include "mk_kernels.h"
+#include "mk_ops.h"
 #include "mk_sched.h"
 
 
@@ -267,6 +268,25 @@ __global__ void keys_to_tokens(const unsigned long long* keys, int n, int32_t* t
 }
 
 }  // namespace
+
+namespace mk {
+
+int op_fail(int code, const char* msg) noexcept {
+  try {
+    g_create_error = msg;
+  } catch (...) {
+  }
+  return code;
+}
+
+int op_cuda(int cuda_error, const char* what) noexcept {
+  if (cuda_error == cudaSuccess) return MK_OK;
+  char msg[256];
+  std::snprintf(msg, sizeof msg, "%s: %s", what, cudaGetErrorString((cudaError_t)cuda_error));
+  return op_fail(cuda_error == cudaErrorMemoryAllocation ? MK_ERR_OOM : MK_ERR_CUDA, msg);
+}
+
+}  // namespace mk
 
 extern "C" {
 

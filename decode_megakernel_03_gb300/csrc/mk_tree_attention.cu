@@ -1,0 +1,693 @@
+// Attention of a tree of drafted tokens over a KV cache (include/mk.h,
+// mk_tree_attention).
+//
+// For kv-head g of sequence b the rows are (node, query head of the group):
+// row r = t * G + i, i < G = n_heads / n_kv_heads. All rows of a (b, g) read the
+// same keys, so a key tile is fetched once for a tile of rows. The tiles of all
+// (b, g) form one line of work that is cut into equal shares, one per group
+// of blocks, wherever the cuts fall; the lengths are read on the device, so the
+// grid does not depend on them and a captured call stays valid. A share that
+// covers a (b, g) whole writes its rows; shares that cover a part write
+// (o, m, l) to the workspace and a second kernel joins them.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "mk_ops.h"
+#include "mk_ptx.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kTile = 64;        // keys of a tile
+constexpr int kStages = 3;       // tiles in shared memory
+constexpr int kThreads = 128;    // four warps, each 16 keys of a tile
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxG = 8;
+
+struct AttnParams {
+  CacheView cache;
+  const uint16_t *k, *v;
+  const void* q;
+  void* out;
+  int64_t qs, os;
+  const int32_t *starts, *parents, *counts;
+  int B, T, nh, G;
+  int row_tiles, groups;  // grid = groups x row_tiles, row tiles fastest
+  float scale_log2;       // scale * log2(e)
+  float* part_o;          // [groups][2][row_tiles][RT][D]
+  float* part_ml;         // [groups][2][row_tiles][RT][2]
+};
+
+// ---- the line of work -----------------------------------------------------------
+// Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), their
+// tiles in order.
+
+struct Item {
+  int b, g, t0, nt;       // nt: tiles of the item; t0: the first tile of this share
+  int64_t first;          // number of the item's tile 0 on the line
+};
+
+__device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
+  const int n = clamped(p.counts, b, p.T);
+  if (n == 0) return 0;
+  return min(clamped(p.starts, b, p.cache.capacity) + n, p.cache.capacity);
+}
+
+// Fills prefix[0..B] (tiles of the sequences before b, times n_kv) with one warp.
+__device__ __forceinline__ void work_line(const AttnParams& p, int64_t* prefix) {
+  const int lane = threadIdx.x % 32;
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t x = b < p.B ? (int64_t)((keys_of(p, b) + kTile - 1) / kTile) * p.cache.n_kv : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (b < p.B) prefix[b + 1] = sum + x;
+    sum += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) prefix[0] = 0;
+  __syncwarp();
+}
+
+// the group whose share holds tile u of a line of W tiles
+__device__ __forceinline__ int group_of(int64_t u, int64_t W, int groups) {
+  return (int)(((u + 1) * groups - 1) / W);
+}
+
+// ---- asynchronous 16-byte copies ---------------------------------------------------
+// (bytes 0: the destination is zeroed)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+// P bf16 parts of a pair whose sum is the value to 2^-8P of it, each part the
+// rounded rest of the ones before (an infinite part has no rest).
+template <int P>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    part[i] = bf16x2_rn(a, b);
+    if (i + 1 < P) {
+      const float ha = bf_lo(part[i]), hb = bf_hi(part[i]);
+      a = isinf(ha) ? 0.f : a - ha;
+      b = isinf(hb) ? 0.f : b - hb;
+    }
+  }
+}
+
+// ---- the kernel ------------------------------------------------------------------------
+// MT m16 row blocks per row tile; P = 1: bf16 activations; P = 3: fp32 ones,
+// queries and weights as three bf16 parts (2^-24 of the value: fp32's own
+// step; the cache is bf16, so products of parts are exact).
+// Weights of bf16 calls are rounded to bf16 (relative 2^-8, the size of the
+// output's own rounding); sums, maxima and the output accumulate in fp32.
+template <int D, int MT, int P>
+struct Layout {
+  static constexpr int RT = 16 * MT;
+  static constexpr int kStageBytes = 2 * kTile * D * 2;
+  static constexpr int kRing = kStages * kStageBytes;
+  // joined warps: o [4][RT][D] fp32 over the ring
+  static_assert(4 * RT * D * 4 <= kRing, "the warps' shares fit the ring");
+  static constexpr int kRowTab = (kStages + 1) * kTile * 4;
+  static constexpr int kBytes = kRing + kRowTab;
+};
+
+template <int D, int MT, int P>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+tree_attention_kernel(const __grid_constant__ AttnParams p) {
+  using Lay = Layout<D, MT, P>;
+  constexpr int RT = Lay::RT, KB = D / 16, NB = D / 8;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint32_t* rowtab = reinterpret_cast<uint32_t*>(smem + Lay::kRing);  // [kStages + 1][kTile]
+  __shared__ int64_t prefix[kMaxSeqs + 1];
+  __shared__ uint64_t s_seen[MK_MAX_TREE];   // node -> the nodes it sees
+  __shared__ int s_up[MK_MAX_TREE];
+  // non-finite values of the nodes' v rows: bit d % 32 of word d / 32, +inf in
+  // [0], -inf in [1], NaN in both
+  __shared__ uint32_t s_odd[MK_MAX_TREE][2][D / 32];
+  __shared__ float s_ml[4][RT][2];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int grp = lane / 4, tig = lane % 4;
+  const int rt = blockIdx.x % p.row_tiles, group = blockIdx.x / p.row_tiles;
+  const uint32_t ring = smem_u32(smem);
+
+  griddep_launch();
+  if (warp == 0) work_line(p, prefix);
+  __syncthreads();
+  const int64_t W = prefix[p.B];
+  int64_t u = group * W / p.groups;
+  const int64_t u_begin = u, u_end = (int64_t)(group + 1) * W / p.groups;
+
+  while (u < u_end) {
+    // the item of tile u: the last sequence whose prefix is <= u
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (prefix[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    const int b = lo;
+    const int nt = (int)((prefix[b + 1] - prefix[b]) / p.cache.n_kv);
+    const int g = (int)((u - prefix[b]) / nt);
+    const int64_t item0 = prefix[b] + (int64_t)g * nt;
+    const int k0 = (int)(u - item0);
+    const int n = (int)min((int64_t)(nt - k0), u_end - u);  // tiles of this share
+    const bool begins = u == u_begin;
+    u += n;
+    const int count = clamped(p.counts, b, p.T);
+    const int start = clamped(p.starts, b, p.cache.capacity);
+    const int len = min(start + count, p.cache.capacity);
+    const int rows = count * p.G;
+    if (rt * RT >= rows) continue;  // no row of this tile is there
+
+    // ---- key rows of tile `it` of the share into rowtab, its copies
+    auto row_of = [&](int it) -> uint32_t {  // threads 0..kTile-1
+      const int slot = (k0 + it) * kTile + tid;
+      if (it >= n || slot >= len) return kNoRow;
+      const uint32_t r = cache_row(p.cache, b, slot);
+      return r == kNoRow ? r : r + (uint32_t)g * p.cache.block_size;
+    };
+    auto fetch = [&](int it) {
+      if (it < n) {
+        constexpr int CPR = D / 8, RPP = kThreads / CPR;
+        const uint32_t* tab = rowtab + it % (kStages + 1) * kTile;
+        const uint32_t base = ring + it % kStages * Lay::kStageBytes;
+        const int c = tid % CPR;
+#pragma unroll
+        for (int i = 0; i < kTile / RPP; ++i) {
+          const int r = tid / CPR + i * RPP;
+          const uint32_t row = tab[r];
+          const uint32_t bytes = row == kNoRow ? 0 : 16;
+          const size_t off = row == kNoRow ? 0 : (size_t)row * D + 8 * c;
+          const uint32_t dst = base + r * (D * 2) + ((c ^ (r & 7)) * 16);
+          cp_async16(dst, p.k + off, bytes);
+          cp_async16(dst + kTile * D * 2, p.v + off, bytes);
+        }
+      }
+      cp_async_commit();
+    };
+
+    __syncthreads();  // the share before this one is done with shared memory
+    if (tid < kTile) {
+#pragma unroll
+      for (int it = 0; it < kStages; ++it) rowtab[it * kTile + tid] = row_of(it);
+    }
+    if (tid < MK_MAX_TREE) {
+      // The nodes each node sees, by doubling: seen covers the nearest 2^i
+      // ancestors, up is the next one behind them.
+      int up = -1;
+      if (tid < count) {
+        up = p.parents ? __ldg(p.parents + (size_t)b * p.T + tid) : tid - 1;
+        if (up < 0 || up >= tid) up = -1;
+      }
+      s_up[tid] = up;
+      s_seen[tid] = 1ull << tid;
+      for (int w = 0; w < 2 * (D / 32); ++w) (&s_odd[tid][0][0])[w] = 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < kStages - 1; ++it) fetch(it);
+    for (int i = 0; i < 6; ++i) {
+      uint64_t seen = 0;
+      int up = -1;
+      if (tid < MK_MAX_TREE) {
+        up = s_up[tid];
+        seen = s_seen[tid];
+        if (up >= 0) {
+          seen |= s_seen[up];
+          up = s_up[up];
+        }
+      }
+      __syncthreads();
+      if (tid < MK_MAX_TREE) {
+        s_up[tid] = up;
+        s_seen[tid] = seen;
+      }
+      __syncthreads();
+    }
+
+    // ---- the rows' queries as A fragments, and what they see
+    uint4 qf[P][MT][KB];
+    uint64_t seen[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const void* src[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = rt * RT + m * 16 + h * 8 + grp;
+        const int t = r / p.G;
+        seen[m][h] = r < rows ? s_seen[t] : 0;
+        const int64_t off = ((int64_t)b * p.T + t) * p.qs + (g * p.G + r % p.G) * D;
+        src[h] = r >= rows ? nullptr
+                 : P > 1    ? (const void*)((const float*)p.q + off)
+                           : (const void*)((const uint16_t*)p.q + off);
+      }
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        uint32_t w[P][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // (grp, 2tig), (grp + 8, 2tig), (grp, 2tig + 8), (grp + 8, 2tig + 8)
+          const int c = kb * 16 + 2 * tig + (j / 2) * 8;
+          const void* s = src[j % 2];
+          if constexpr (P > 1) {
+            const float2 x = s ? __ldg((const float2*)((const float*)s + c)) : make_float2(0.f, 0.f);
+            uint32_t part[P];
+            split(x.x, x.y, part);
+#pragma unroll
+            for (int q = 0; q < P; ++q) w[q][j] = part[q];
+          } else {
+            w[0][j] = s ? __ldg((const uint32_t*)((const uint16_t*)s + c)) : 0u;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < P; ++q) qf[q][m][kb] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+      }
+    }
+
+    float o[MT][NB][4], mx[MT][2], sum[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int d = 0; d < NB; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[m][d][e] = 0.f;
+      mx[m][0] = mx[m][1] = -INFINITY;
+      sum[m][0] = sum[m][1] = 0.f;
+    }
+
+    // ---- the tiles
+    for (int it = 0; it < n; ++it) {
+      cp_async_wait<kStages - 2>();
+      __syncthreads();  // tile `it` is there; everybody is done with tile it - 1
+      fetch(it + kStages - 1);
+      uint32_t next_row = kNoRow;
+      if (tid < kTile) next_row = row_of(it + kStages);
+      const uint32_t ks = ring + it % kStages * Lay::kStageBytes, vs = ks + kTile * D * 2;
+      const uint32_t* tab = rowtab + it % (kStages + 1) * kTile;
+      const int slot0 = (k0 + it) * kTile;
+
+      bool odd = false;  // the tile holds a node with a non-finite v value
+      if (slot0 + kTile > start) {
+        // nodes of the tile: a value that some rows must not see cannot be
+        // cancelled by a zero weight if it is not finite, so it is taken out
+        // here and added to the rows that see it
+        constexpr int CPR = D / 8;
+        bool bad = false;
+        for (int i = tid; i < kTile * CPR; i += kThreads) {
+          const int r = i / CPR, c = i % CPR, node = slot0 + r - start;
+          if (node < 0 || node >= count || tab[r] == kNoRow) continue;
+          uint8_t* at = smem + (vs - ring) + r * (D * 2) + ((c ^ (r & 7)) * 16);
+          uint16_t* x = reinterpret_cast<uint16_t*>(at);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint16_t v = x[e];
+            if ((v & 0x7f80) == 0x7f80) {
+              const int d = c * 8 + e;
+              const bool nan = v & 0x7f;
+              if (nan || !(v & 0x8000)) atomicOr(&s_odd[node][0][d / 32], 1u << (d % 32));
+              if (nan || (v & 0x8000)) atomicOr(&s_odd[node][1][d / 32], 1u << (d % 32));
+              x[e] = 0;
+              bad = true;
+            }
+          }
+        }
+        odd = __syncthreads_or(bad);
+      }
+
+      // scores of the warp's 16 keys
+      float s[MT][2][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[m][j][e] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        // blocks: keys 0-7 dims 0-7, keys 0-7 dims 8-15, keys 8-15 dims 0-7, ...
+        const int r = warp * 16 + (lane / 16) * 8 + lane % 8, c = kb * 2 + (lane / 8) % 2;
+        uint32_t kf[4];
+        ldsm_x4(kf, ks + r * (D * 2) + ((c ^ (r & 7)) * 16));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            mma_bf16_16816(s[m][0], qf[q][m][kb], kf[0], kf[1]);
+            mma_bf16_16816(s[m][1], qf[q][m][kb], kf[2], kf[3]);
+          }
+      }
+      // what is not seen: keys behind the length, pages that are not there,
+      // nodes that are no ancestors
+      const uint32_t mine = lane < 16 ? tab[warp * 16 + lane] : 0;
+      const bool plain = slot0 + kTile <= start && !__any_sync(0xffffffffu, mine == kNoRow);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[m][j][e] *= p.scale_log2;
+            if (!plain) {
+              const int key = warp * 16 + j * 8 + 2 * tig + (e & 1);
+              const int node = slot0 + key - start;
+              const bool see = tab[key] != kNoRow && (node < 0 || (seen[m][e / 2] >> node & 1));
+              if (!see) s[m][j][e] = -INFINITY;
+            }
+          }
+
+      // running maximum and sum
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float t = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]),
+                          fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+          const float now = fmaxf(mx[m][h], t);
+          const float from = now == -INFINITY ? 0.f : now;  // nothing seen yet: weights 0
+          const float keep = fast_exp2(mx[m][h] - from);
+          mx[m][h] = now;
+          float add = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float w = fast_exp2(s[m][j][2 * h + e] - from);
+              s[m][j][2 * h + e] = w;
+              add += w;
+            }
+          sum[m][h] = sum[m][h] * keep + add;
+          if (__any_sync(0xffffffffu, keep != 1.f)) {
+#pragma unroll
+            for (int d = 0; d < NB; ++d) {
+              o[m][d][2 * h] *= keep;
+              o[m][d][2 * h + 1] *= keep;
+            }
+          }
+        }
+
+      // o += weights x v
+      uint4 w[P][MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t x[4][P];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split(s[m][j / 2][j % 2 * 2], s[m][j / 2][j % 2 * 2 + 1], x[j]);
+#pragma unroll
+        for (int q = 0; q < P; ++q) w[q][m] = make_uint4(x[0][q], x[1][q], x[2][q], x[3][q]);
+      }
+#pragma unroll
+      for (int d = 0; d < NB; d += 2) {
+        const int r = warp * 16 + (lane / 8) % 2 * 8 + lane % 8, c = d + lane / 16;
+        uint32_t vf[4];
+        ldsm_x4_t(vf, vs + r * (D * 2) + ((c ^ (r & 7)) * 16));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            mma_bf16_16816(o[m][d], w[q][m], vf[0], vf[1]);
+            mma_bf16_16816(o[m][d + 1], w[q][m], vf[2], vf[3]);
+          }
+      }
+      if (odd) {
+#pragma unroll 1
+        for (int key = warp * 16; key < warp * 16 + 16; ++key) {
+          const int node = slot0 + key - start;
+          if (node < 0 || node >= count || tab[key] == kNoRow) continue;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int d = 0; d < NB; ++d)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int c = d * 8 + 2 * tig + (e & 1);
+                if (!(seen[m][e / 2] >> node & 1)) continue;
+                if (s_odd[node][0][c / 32] >> (c % 32) & 1) o[m][d][e] += INFINITY;
+                if (s_odd[node][1][c / 32] >> (c % 32) & 1) o[m][d][e] -= INFINITY;
+              }
+        }
+      }
+      if (tid < kTile) rowtab[(it + kStages) % (kStages + 1) * kTile + tid] = next_row;
+    }
+
+    // ---- the warps' shares joined: sums within a quad, maxima across warps
+    cp_async_wait<0>();
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 1);
+        sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 2);
+        if (tig == 0) {
+          s_ml[warp][m * 16 + h * 8 + grp][0] = mx[m][h];
+          s_ml[warp][m * 16 + h * 8 + grp][1] = sum[m][h];
+        }
+      }
+    __syncthreads();  // also: everybody is done with the ring
+    float* so = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = m * 16 + h * 8 + grp;
+        const float top = fmaxf(fmaxf(s_ml[0][r][0], s_ml[1][r][0]), fmaxf(s_ml[2][r][0], s_ml[3][r][0]));
+        const float f = fast_exp2(mx[m][h] - top);
+        const bool none = sum[m][h] == 0.f;  // a seen key's largest weight is 1 (or NaN)
+#pragma unroll
+        for (int d = 0; d < NB; ++d)
+          *reinterpret_cast<float2*>(so + (warp * RT + r) * D + d * 8 + 2 * tig) =
+              none ? make_float2(0.f, 0.f) : make_float2(o[m][d][2 * h] * f, o[m][d][2 * h + 1] * f);
+      }
+    __syncthreads();
+    const bool whole = n == nt;
+    const size_t slot = ((size_t)group * 2 + (begins ? 0 : 1)) * p.row_tiles + rt;
+    for (int i = tid; i < RT * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = i % (D / 4) * 4, row = rt * RT + r;
+      if (row >= rows) break;
+      const float top = fmaxf(fmaxf(s_ml[0][r][0], s_ml[1][r][0]), fmaxf(s_ml[2][r][0], s_ml[3][r][0]));
+      float l = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w4 = 0; w4 < 4; ++w4) {
+        if (s_ml[w4][r][1] != 0.f) l += s_ml[w4][r][1] * fast_exp2(s_ml[w4][r][0] - top);
+        const float4 x = *reinterpret_cast<const float4*>(so + (w4 * RT + r) * D + c);
+        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+      }
+      if (whole) {
+        const float f = l == 0.f ? 0.f : 1.f / l;  // no key seen: 0
+        if (l == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);
+        a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+        const int64_t off = ((int64_t)b * p.T + row / p.G) * p.os + (g * p.G + row % p.G) * D + c;
+        if constexpr (P > 1)
+          *reinterpret_cast<float4*>((float*)p.out + off) = a;
+        else
+          *reinterpret_cast<uint2*>((uint16_t*)p.out + off) =
+              make_uint2(bf16x2_rn(a.x, a.y), bf16x2_rn(a.z, a.w));
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (slot * RT + r) * D + c) = a;
+        if (c == 0) {
+          p.part_ml[(slot * RT + r) * 2] = top;
+          p.part_ml[(slot * RT + r) * 2 + 1] = l;
+        }
+      }
+    }
+  }
+}
+
+// Joins the shares of the items that were cut: a warp takes one row, each lane
+// D / 32 of its columns; the shares follow one another in the order of the line.
+template <int D, int RT, typename T>
+__global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ AttnParams p) {
+  constexpr int E = D / 32;
+  __shared__ int64_t prefix[kMaxSeqs + 1];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int b = blockIdx.y / p.cache.n_kv, g = blockIdx.y % p.cache.n_kv;
+  if (warp == 0) work_line(p, prefix);
+  __syncthreads();
+  griddep_wait();
+  const int row = blockIdx.x * 4 + warp, count = clamped(p.counts, b, p.T);
+  const int64_t W = prefix[p.B];
+  const int nt = (int)((prefix[b + 1] - prefix[b]) / p.cache.n_kv);
+  if (nt == 0 || row >= count * p.G) return;
+  const int64_t item0 = prefix[b] + (int64_t)g * nt;
+  const int g0 = group_of(item0, W, p.groups), g1 = group_of(item0 + nt - 1, W, p.groups);
+  if (g0 == g1) return;  // written whole
+  const int rt = row / RT, r = row % RT;
+  float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int s = g0; s <= g1; ++s) {
+    const int64_t u0 = s * W / p.groups, u1 = (int64_t)(s + 1) * W / p.groups;
+    if (u0 == u1) continue;  // more groups than tiles
+    const size_t at = (((size_t)s * 2 + (u0 < item0 ? 1 : 0)) * p.row_tiles + rt) * RT + r;
+    const float ms = p.part_ml[at * 2], ls = p.part_ml[at * 2 + 1];
+    if (ls == 0.f) continue;  // no key of this share is seen
+    const float now = fmaxf(m, ms), keep = fast_exp2(m - now), f = fast_exp2(ms - now);
+    m = now;
+    l = l * keep + ls * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p.part_o[at * D + lane * E + e] * f;
+  }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  const int64_t off = ((int64_t)b * p.T + row / p.G) * p.os + (g * p.G + row % p.G) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float x = l == 0.f ? 0.f : o[e] * f, y = l == 0.f ? 0.f : o[e + 1] * f;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>((float*)p.out + off + e) = make_float2(x, y);
+    else
+      *reinterpret_cast<uint32_t*>((uint16_t*)p.out + off + e) = bf16x2_rn(x, y);
+  }
+}
+
+struct Plan {
+  int row_tile, row_tiles, groups;
+  size_t o_floats, ml_floats;
+};
+
+// Rows per tile: 32 for bf16 activations with more than 16 rows; fp32 ones keep
+// three parts of every query in registers, which leaves room for 16 rows.
+Plan plan_of(int T, int G, int D, int type, int n_sm) {
+  Plan pl;
+  pl.row_tile = type == MK_TYPE_BF16 && T * G > 16 ? 32 : 16;
+  pl.row_tiles = (T * G + pl.row_tile - 1) / pl.row_tile;
+  pl.groups = std::max(1, kCtasPerSm * n_sm / pl.row_tiles);
+  const size_t rows = (size_t)pl.groups * 2 * pl.row_tiles * pl.row_tile;
+  pl.o_floats = rows * D;
+  pl.ml_floats = rows * 2;
+  return pl;
+}
+
+int check_attention(const mk_cache* cache, int batch, int n_tokens, int n_heads, int type,
+                    CacheView* view) {
+  if (int rc = check_cache(cache, batch, true, view)) return rc;
+  if (n_tokens < 1 || n_tokens > MK_MAX_TREE)
+    return op_fail(MK_ERR_INVALID, "n_tokens must be 1 to MK_MAX_TREE");
+  if (type != MK_TYPE_BF16 && type != MK_TYPE_FP32)
+    return op_fail(MK_ERR_INVALID, "type must be MK_TYPE_BF16 or MK_TYPE_FP32");
+  if (cache->n_kv_heads > 4096 || (int64_t)batch * cache->n_kv_heads > 65535)
+    return op_fail(MK_ERR_INVALID, "batch x n_kv_heads must be at most 65535");
+  if (n_heads < 1 || n_heads % cache->n_kv_heads || n_heads / cache->n_kv_heads > kMaxG)
+    return op_fail(MK_ERR_INVALID,
+                   "n_heads must be a multiple of n_kv_heads, at most 8 heads per kv-head");
+  return MK_OK;
+}
+
+int make_plan(const mk_cache* cache, int n_tokens, int n_heads, int type, Plan* pl) {
+  int device = 0, n_sm = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  *pl = plan_of(n_tokens, n_heads / cache->n_kv_heads, cache->head_dim, type, n_sm);
+  return MK_OK;
+}
+
+template <int D, int MT, int P>
+int launch(const AttnParams& p, cudaStream_t st) {
+  using Lay = Layout<D, MT, P>;
+  auto* fn = tree_attention_kernel<D, MT, P>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
+  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  fn<<<p.groups * p.row_tiles, kThreads, Lay::kBytes, st>>>(p);
+  if (int rc = op_cuda(cudaGetLastError(), "mk_tree_attention")) return rc;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.T * p.G + 3) / 4, p.B * p.cache.n_kv);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  using T = typename std::conditional<(P > 1), float, uint16_t>::type;
+  return op_cuda(cudaLaunchKernelEx(&cfg, tree_attention_join<D, Lay::RT, T>, p),
+                 "mk_tree_attention");
+}
+
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" {
+
+int mk_tree_attention_workspace(const mk_cache* cache, int batch, int n_tokens, int n_heads,
+                                int type, size_t* bytes) {
+  if (!bytes) return op_fail(MK_ERR_INVALID, "bytes is NULL");
+  CacheView view;
+  Plan pl;
+  if (int rc = check_attention(cache, batch, n_tokens, n_heads, type, &view)) return rc;
+  if (int rc = make_plan(cache, n_tokens, n_heads, type, &pl)) return rc;
+  *bytes = (pl.o_floats + pl.ml_floats) * sizeof(float);
+  return MK_OK;
+}
+
+int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
+                      int type, float scale, const void* q, int64_t q_stride,
+                      const int32_t* starts, const int32_t* parents, const int32_t* counts,
+                      void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  AttnParams p;
+  Plan pl;
+  if (int rc = check_attention(cache, batch, n_tokens, n_heads, type, &p.cache)) return rc;
+  if (layer < 0 || layer >= cache->n_layers)
+    return op_fail(MK_ERR_INVALID, "layer out of range [0, n_layers)");
+  if (!q || !out || !starts || !workspace)
+    return op_fail(MK_ERR_INVALID, "mk_tree_attention: a NULL argument");
+  if (!(scale > 0.f) || scale > 1e30f)
+    return op_fail(MK_ERR_INVALID, "scale must be positive and finite");
+  const int unit = type == MK_TYPE_FP32 ? 4 : 8;
+  const int64_t row = (int64_t)n_heads * cache->head_dim;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_stride % unit || out_stride % unit ||
+      q_stride < row || out_stride < row)
+    return op_fail(MK_ERR_INVALID,
+                   "q, out: 16-byte aligned rows, strides at least a row, are needed");
+  if (!aligned(workspace, 256)) return op_fail(MK_ERR_INVALID, "workspace: not 256-byte aligned");
+  if (int rc = make_plan(cache, n_tokens, n_heads, type, &pl)) return rc;
+  if (workspace_bytes < (pl.o_floats + pl.ml_floats) * sizeof(float))
+    return op_fail(MK_ERR_INVALID, "workspace: smaller than its query says");
+  p.k = (const uint16_t*)cache->k[layer];
+  p.v = (const uint16_t*)cache->v[layer];
+  p.q = q, p.out = out, p.qs = q_stride, p.os = out_stride;
+  p.starts = starts, p.parents = parents, p.counts = counts;
+  p.B = batch, p.T = n_tokens, p.nh = n_heads, p.G = n_heads / cache->n_kv_heads;
+  p.row_tiles = pl.row_tiles, p.groups = pl.groups;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.part_o = (float*)workspace;
+  p.part_ml = p.part_o + pl.o_floats;
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool wide = pl.row_tile == 32;
+  if (cache->head_dim == 64) {
+    if (type == MK_TYPE_FP32) return launch<64, 1, 3>(p, st);
+    return wide ? launch<64, 2, 1>(p, st) : launch<64, 1, 1>(p, st);
+  }
+  if (type == MK_TYPE_FP32) return launch<128, 1, 3>(p, st);
+  return wide ? launch<128, 2, 1>(p, st) : launch<128, 1, 1>(p, st);
+}
+
+}  // extern "C"

@@ -26,7 +26,12 @@ EXPORTS = ("mk_create", "mk_decode_step", "mk_decode_step_multilaunch", "mk_get_
            "mk_decode_step_noalloc", "mk_debug_use_generic_kernel", "mk_decode_greedy",
            "mk_create_paged", "mk_decode_step_paged", "mk_decode_greedy_persistent",
            "mk_debug_permute_queues", "mk_set_dynamic", "mk_schedule_build_dynamic",
-           "mk_schedule_build_steps", "mk_prefill")
+           "mk_schedule_build_steps", "mk_prefill",
+           # operators over a KV cache
+           "mk_rope_init", "mk_rope_append", "mk_tree_attention", "mk_tree_attention_workspace",
+           "mk_tree_accept", "mk_tree_accept_workspace", "mk_cache_compact",
+           "mk_cache_copy_blocks", "mk_pages_create", "mk_pages_destroy", "mk_pages_resize",
+           "mk_pages_fork", "mk_pages_compact", "mk_pages_read")
 
 MAX_STEPS_PER_LAUNCH = 32  # MK_MAX_STEPS_PER_LAUNCH
 
@@ -62,6 +67,28 @@ class MkInstr(ctypes.Structure):
                 ("a1", ctypes.c_int32), ("a2", ctypes.c_int32), ("wait_ctr", ctypes.c_int32),
                 ("wait_target", ctypes.c_int32), ("sig_ctr", ctypes.c_int32),
                 ("sig_amount", ctypes.c_int32)]
+
+
+class MkCache(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("n_blocks", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("batch", ctypes.c_int),
+                ("table_entries", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("k", _vpp), ("v", _vpp)]
+
+
+class MkRopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("theta", ctypes.c_float), ("factor", ctypes.c_float), ("low", ctypes.c_float),
+                ("high", ctypes.c_float), ("original_length", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
+
+
+class MkRope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * 64)]
 
 
 INSTR_DTYPE = np.dtype([("op", "<i2"), ("layer", "<i2"), ("a0", "<i4"), ("a1", "<i4"),
@@ -120,6 +147,25 @@ def lib():
         L.mk_decode_step_noalloc.argtypes = [ctypes.POINTER(MkConfig), ctypes.POINTER(MkWeights),
                                              _vpp, _vpp, i32p, i32p, vp, vp, ctypes.c_char_p,
                                              ctypes.c_size_t]
+        i, i64, size, sizep = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(
+            ctypes.c_size_t)
+        ip, cachep = ctypes.POINTER(ctypes.c_int), ctypes.POINTER(MkCache)
+        L.mk_rope_init.argtypes = [ctypes.POINTER(MkRopeConfig), ctypes.POINTER(MkRope)]
+        L.mk_rope_append.argtypes = [ctypes.POINTER(MkRope), cachep, i, i, i, i, i, vp, i64, vp,
+                                     i64, vp, i64, vp, i64, vp, vp, vp, vp]
+        L.mk_tree_attention.argtypes = [cachep, i, i, i, i, i, ctypes.c_float, vp, i64, vp, vp, vp,
+                                        vp, i64, vp, size, vp]
+        L.mk_tree_attention_workspace.argtypes = [cachep, i, i, i, i, sizep]
+        L.mk_tree_accept.argtypes = [i, i, i, i, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
+        L.mk_tree_accept_workspace.argtypes = [i, i, i, sizep]
+        L.mk_cache_compact.argtypes = [cachep, i, i, vp, vp, vp, vp]
+        L.mk_cache_copy_blocks.argtypes = [cachep, vp, i, vp]
+        L.mk_pages_create.argtypes = [i, i, i, i, ctypes.POINTER(vp)]
+        L.mk_pages_destroy.argtypes = [vp]
+        L.mk_pages_resize.argtypes = [vp, i, vp, vp, vp, i, ip]
+        L.mk_pages_fork.argtypes = [vp, i, vp, vp]
+        L.mk_pages_compact.argtypes = [vp, vp, i, ip]
+        L.mk_pages_read.argtypes = [vp, vp, vp, ip]
         _lib = L
     return _lib
 
@@ -399,6 +445,333 @@ class Decoder:
     def close(self):
         if getattr(self, "h", None):
             lib().mk_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---- operators over a KV cache -------------------------------------------------------
+
+MAX_TREE = 64  # MK_MAX_TREE
+TYPE_BF16, TYPE_FP32 = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}  # MK_ROPE_*
+
+
+def _bad(msg: str) -> MkError:
+    return MkError(MK_ERR_INVALID, msg)
+
+
+class Cache:
+    """A model's KV cache as the operators see it (mk_cache).
+
+    k, v: each layer's bf16 CUDA tensor, contiguous: caches [B][nkv][S][D], or
+    block pools [n_blocks][nkv][block_size][D] with block_table, a contiguous
+    int32 CUDA tensor [batch][entries]. The tensors are updated in place; the
+    table may be rewritten between calls (in stream order).
+    """
+
+    def __init__(self, k: list, v: list, block_table=None):
+        import torch
+        k, v = list(k), list(v)
+        if not k or len(k) != len(v):
+            raise _bad("k and v must hold a tensor for each layer")
+        first = k[0]
+        for t in k + v:
+            if not t.is_cuda or t.dtype != torch.bfloat16 or not t.is_contiguous():
+                raise _bad("k and v must be contiguous CUDA bfloat16 tensors")
+            if t.dim() != 4 or t.shape != first.shape or t.device != first.device:
+                raise _bad("k and v must be [blocks][nkv][block_size][D], alike in every layer")
+        self.n_layers = len(k)
+        self.n_blocks, self.n_kv_heads, self.block_size, self.head_dim = map(int, first.shape)
+        self.device = first.device
+        self.batch, entries, ptr = self.n_blocks, 0, None
+        if block_table is not None:
+            _ints(block_table, 2, self.device, "block_table")
+            self.batch, entries = map(int, block_table.shape)
+            ptr = block_table.data_ptr()
+        self.k, self.v, self.block_table = k, v, block_table
+        n = self.n_layers
+        self._k = (ctypes.c_void_p * n)(*[t.data_ptr() for t in k])
+        self._v = (ctypes.c_void_p * n)(*[t.data_ptr() for t in v])
+        self.struct = MkCache(n, self.n_kv_heads, self.head_dim, self.n_blocks, self.block_size,
+                              self.batch, entries, ptr, ctypes.cast(self._k, _vpp),
+                              ctypes.cast(self._v, _vpp))
+        self.ref = ctypes.byref(self.struct)
+
+
+class Rope:
+    """A plan of rotary positions (mk_rope_init). rotary_dim: the head's first
+    dimensions that turn (default: all); interleaved: pairs (2i, 2i + 1)
+    instead of (i, i + rotary_dim / 2); scaling: "none", "linear", "bands" or
+    "yarn"; magnitude None: 1, or 0.1 ln(factor) + 1 for "yarn"."""
+
+    def __init__(self, head_dim: int, theta: float = 10000.0, rotary_dim: int | None = None,
+                 interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+                 low: float = 1.0, high: float = 4.0, original_length: int = 0,
+                 magnitude: float | None = None):
+        if scaling not in ROPE_SCALINGS:
+            raise _bad(f"scaling must be one of {', '.join(ROPE_SCALINGS)}")
+        if magnitude is not None and not magnitude > 0:
+            raise _bad("magnitude must be positive")
+        cfg = MkRopeConfig(head_dim, head_dim if rotary_dim is None else rotary_dim,
+                           int(bool(interleaved)), ROPE_SCALINGS[scaling], theta, factor, low,
+                           high, original_length, magnitude or 0.0)
+        self.struct = MkRope()
+        self.ref = ctypes.byref(self.struct)
+        _check(lib().mk_rope_init(ctypes.byref(cfg), self.ref))
+
+
+def _raw_stream(stream, device) -> int:
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise _bad("stream and tensors are on different devices")
+    return stream.cuda_stream
+
+
+def _ints(t, dims: int, device, what: str, shape=None) -> int:
+    """The pointer of an int32 index tensor (contiguous, on `device`)."""
+    import torch
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise _bad(f"{what} must be a contiguous int32 tensor on {device}")
+    if t.dim() != dims or (shape is not None and tuple(t.shape) != shape):
+        raise _bad(f"{what} must have the shape {shape if shape else f'of {dims} dimensions'}")
+    return t.data_ptr()
+
+
+def _opt_ints(t, dims, device, what, shape):
+    return None if t is None else _ints(t, dims, device, what, shape)
+
+
+def _type_of(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return TYPE_BF16
+    if t.dtype == torch.float32:
+        return TYPE_FP32
+    raise _bad(f"{what} must be bfloat16 or float32")
+
+
+def _heads(t, shape, dtype, device, what: str) -> int:
+    """The row stride of t [B][T][heads][D]: heads packed, rows evenly spaced."""
+    if t.dtype != dtype or t.device != device or t.dim() != 4:
+        raise _bad(f"{what} must be a {dtype} tensor of 4 dimensions on {device}")
+    if tuple(t.shape) != shape:
+        raise _bad(f"{what} has the shape {tuple(t.shape)}, not {shape}")
+    b, n, h, d = shape
+    sb, sn, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != d):
+        raise _bad(f"{what}: a row's heads must be packed")
+    if n == 1:
+        return sb if b > 1 else h * d
+    if b > 1 and sb != n * sn:
+        raise _bad(f"{what}: rows must be evenly spaced over batch and tokens")
+    return sn
+
+
+def _on_device(device):
+    """Makes `device` current for the launch when it is not."""
+    import contextlib
+
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=None, counts=None,
+                q_out=None, stream=None):
+    """mk_rope_append: q [B][T][nh][D], k, v [B][T][nkv][D] (bf16 or fp32; views
+    into a fused projection's rows are fine), starts [B], parents [B][T],
+    counts [B] int32, all on the device. Returns the rotated queries (q_out,
+    which may be q; else a new tensor, whose rows behind counts are 0)."""
+    import torch
+    dev = cache.device
+    if q.dim() != 4:
+        raise _bad("q must be [batch][tokens][heads][head_dim]")
+    b, n, nh, d = q.shape
+    kind, dtype = _type_of(q, "q"), q.dtype
+    if d != cache.head_dim:
+        raise _bad("q's head_dim is not the cache's")
+    kv = (b, n, cache.n_kv_heads, d)
+    qs = _heads(q, (b, n, nh, d), dtype, dev, "q")
+    ks, vs = _heads(k, kv, dtype, dev, "k"), _heads(v, kv, dtype, dev, "v")
+    sp = _ints(starts, 1, dev, "starts", (b,))
+    pp = _opt_ints(parents, 2, dev, "parents", (b, n))
+    cp = _opt_ints(counts, 1, dev, "counts", (b,))
+    st = _raw_stream(stream, dev)
+    with _on_device(dev):
+        if q_out is None:
+            q_out = _new(torch.empty if counts is None else torch.zeros, (b, n, nh, d), dtype, dev,
+                         stream)
+        os_ = _heads(q_out, (b, n, nh, d), dtype, dev, "q_out")
+        _check(lib().mk_rope_append(rope.ref, cache.ref, layer, b, n, nh, kind, q.data_ptr(), qs,
+                                    k.data_ptr(), ks, v.data_ptr(), vs, q_out.data_ptr(), os_, sp,
+                                    pp, cp, st))
+    return q_out
+
+
+def _new(make, shape, dtype, device, stream):
+    """A tensor that belongs to `stream` (None: the current one)."""
+    import torch
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def tree_attention(cache: Cache, layer: int, q, starts, parents=None, counts=None, scale=None,
+                   out=None, stream=None):
+    """mk_tree_attention: q [B][T][nh][D] (bf16 or fp32) over `layer` of the
+    cache, whose slots starts[b] + t hold the nodes' rows. scale None:
+    1 / sqrt(D). Returns out (given, or new; new rows behind counts are 0). The
+    workspace is allocated for the call on its stream."""
+    import torch
+    dev = cache.device
+    if q.dim() != 4:
+        raise _bad("q must be [batch][tokens][heads][head_dim]")
+    shape = b, n, nh, d = tuple(q.shape)
+    kind, dtype = _type_of(q, "q"), q.dtype
+    if d != cache.head_dim:
+        raise _bad("q's head_dim is not the cache's")
+    qs = _heads(q, shape, dtype, dev, "q")
+    sp = _ints(starts, 1, dev, "starts", (b,))
+    pp = _opt_ints(parents, 2, dev, "parents", (b, n))
+    cp = _opt_ints(counts, 1, dev, "counts", (b,))
+    st = _raw_stream(stream, dev)
+    with _on_device(dev):
+        size = ctypes.c_size_t()
+        _check(lib().mk_tree_attention_workspace(cache.ref, b, n, nh, kind, ctypes.byref(size)))
+        ws = _new(torch.empty, size.value, torch.uint8, dev, stream)
+        if out is None:
+            out = _new(torch.empty if counts is None else torch.zeros, shape, dtype, dev, stream)
+        os_ = _heads(out, shape, dtype, dev, "out")
+        _check(lib().mk_tree_attention(cache.ref, layer, b, n, nh, kind,
+                                       d ** -0.5 if scale is None else scale, q.data_ptr(), qs, sp,
+                                       pp, cp, out.data_ptr(), os_, ws.data_ptr(), size.value, st))
+    return out
+
+
+def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
+    """mk_tree_accept: logits [B][T][V] (bf16 or fp32), tokens [B][T] int32.
+    Returns int32 (choices [B][T], path [B][T], accepted [B], next [B])."""
+    import torch
+    dev = logits.device
+    if not logits.is_cuda or logits.dim() != 3:
+        raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
+    kind = _type_of(logits, "logits")
+    b, n, vocab = logits.shape
+    sb, sn, sv = logits.stride()
+    stride = (sb if b > 1 else vocab) if n == 1 else sn
+    if (vocab > 1 and sv != 1) or (n > 1 and b > 1 and sb != n * sn):
+        raise _bad("logits: rows must be packed and evenly spaced")
+    tp = _ints(tokens, 2, dev, "tokens", (b, n))
+    pp = _opt_ints(parents, 2, dev, "parents", (b, n))
+    cp = _opt_ints(counts, 1, dev, "counts", (b,))
+    st = _raw_stream(stream, dev)
+    with _on_device(dev):
+        size = ctypes.c_size_t()
+        _check(lib().mk_tree_accept_workspace(b, n, vocab, ctypes.byref(size)))
+        ws = _new(torch.empty, size.value, torch.uint8, dev, stream)
+        choices, path, accepted, last = (_new(torch.empty, s, torch.int32, dev, stream)
+                                         for s in ((b, n), (b, n), (b,), (b,)))
+        _check(lib().mk_tree_accept(b, n, vocab, kind, logits.data_ptr(), stride, tp, pp, cp,
+                                    choices.data_ptr(), path.data_ptr(), accepted.data_ptr(),
+                                    last.data_ptr(), ws.data_ptr(), size.value, st))
+    return choices, path, accepted, last
+
+
+def cache_compact(cache: Cache, starts, path, accepted, stream=None):
+    """mk_cache_compact: the accepted nodes' rows moved down behind the context
+    in every layer; starts [B], path [B][T], accepted [B] as tree_accept gives
+    them."""
+    dev = cache.device
+    b = starts.shape[0]
+    sp = _ints(starts, 1, dev, "starts")
+    pp = _ints(path, 2, dev, "path")
+    if path.shape[0] != b:
+        raise _bad("path must have a row for each sequence")
+    ap = _ints(accepted, 1, dev, "accepted", (b,))
+    st = _raw_stream(stream, dev)
+    with _on_device(dev):
+        _check(lib().mk_cache_compact(cache.ref, b, path.shape[1], sp, pp, ap, st))
+
+
+def cache_copy_blocks(cache: Cache, copies, stream=None):
+    """mk_cache_copy_blocks: copies [n][3] on the host, (src, dst, rows) each, as
+    the calls of Pages return them."""
+    c = np.ascontiguousarray(copies, dtype=np.int32)
+    if c.size and (c.ndim != 2 or c.shape[1] != 3):
+        raise _bad("copies must be [n][3]")
+    st = _raw_stream(stream, cache.device)
+    with _on_device(cache.device):
+        _check(lib().mk_cache_copy_blocks(cache.ref, c.ctypes.data, c.size // 3, st))
+
+
+class Pages:
+    """The page tables of a paged cache, on the host (mk_pages_*): which blocks
+    each of n_seqs sequences holds. resize and compact return the copies
+    ([n][3] int32) that cache_copy_blocks has to make before the pages are
+    written; table() is what Decoder.step_paged takes."""
+
+    def __init__(self, n_blocks: int, block_size: int, n_seqs: int, kv_capacity: int):
+        self.h = ctypes.c_void_p()
+        self.n_blocks, self.n_seqs = n_blocks, n_seqs
+        _check(lib().mk_pages_create(n_blocks, block_size, n_seqs, kv_capacity,
+                                     ctypes.byref(self.h)))
+        self.entries = -(-kv_capacity // block_size)
+
+    @staticmethod
+    def _pair(a, b, what: str):
+        a, b = (np.ascontiguousarray(np.atleast_1d(x), dtype=np.int32) for x in (a, b))
+        if a.ndim != 1 or a.shape != b.shape:
+            raise _bad(f"{what} must be two lists of the same length")
+        return a, b
+
+    def resize(self, seqs, lengths) -> np.ndarray:
+        """mk_pages_resize (0: gives a sequence's pages back)."""
+        s, n = self._pair(seqs, lengths, "seqs, lengths")
+        copies, made = np.empty((len(s), 3), np.int32), ctypes.c_int()
+        _check(lib().mk_pages_resize(self.h, len(s), s.ctypes.data, n.ctypes.data,
+                                     copies.ctypes.data, len(s), ctypes.byref(made)))
+        return copies[:made.value]
+
+    def fork(self, parents, children):
+        """mk_pages_fork: each empty child becomes a fork of its parent."""
+        p, c = self._pair(parents, children, "parents, children")
+        _check(lib().mk_pages_fork(self.h, len(p), p.ctypes.data, c.ctypes.data))
+
+    def compact(self) -> np.ndarray:
+        """mk_pages_compact: the pages in use renumbered to the lowest ones."""
+        copies, made = np.empty((self.n_blocks, 3), np.int32), ctypes.c_int()
+        _check(lib().mk_pages_compact(self.h, copies.ctypes.data, self.n_blocks,
+                                      ctypes.byref(made)))
+        return copies[:made.value]
+
+    def table(self) -> np.ndarray:
+        """[n_seqs][entries] int32, -1 behind a sequence's pages."""
+        t = np.empty((self.n_seqs, self.entries), np.int32)
+        _check(lib().mk_pages_read(self.h, t.ctypes.data, None, None))
+        return t
+
+    def lengths(self) -> np.ndarray:
+        n = np.empty(self.n_seqs, np.int32)
+        _check(lib().mk_pages_read(self.h, None, n.ctypes.data, None))
+        return n
+
+    def n_free(self) -> int:
+        n = ctypes.c_int()
+        _check(lib().mk_pages_read(self.h, None, None, ctypes.byref(n)))
+        return n.value
+
+    def close(self):
+        if getattr(self, "h", None):
+            lib().mk_pages_destroy(self.h)
             self.h = None
 
     def __del__(self):

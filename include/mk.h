@@ -191,8 +191,9 @@ int mk_get_status(mk_handle* h, void* stream);
    Accepts NULL. */
 int mk_destroy(mk_handle* h);
 
-/* Human-readable description of the last error on h (or of the last
-   mk_create failure in this thread when h is NULL). Never NULL. */
+/* Human-readable description of the last error on h (or, when h is NULL, of
+   this thread's last failure of mk_create or of a call that takes no handle).
+   Never NULL. */
 const char* mk_last_error(const mk_handle* h);
 
 /* ---- test / benchmark helpers ------------------------------------------ */
@@ -324,6 +325,196 @@ int mk_schedule_build_steps(const mk_config* cfg, int n_sm, const int32_t* posit
                             mk_instr* instrs, int instr_capacity, int* n_instr,
                             int32_t* sm_offsets, int32_t* targets, int counter_capacity,
                             int* n_counters);
+
+/* ---- operators over a KV cache ------------------------------------------- */
+
+/* What a serving loop needs beside the decode step, on the same caches: a
+   tree of drafted tokens verified in one pass (new rows appended with rotary
+   positions, attention of the tree's nodes, greedy acceptance, the accepted
+   rows moved down behind the context), and the pages of a paged cache forked,
+   copied, compacted and freed.
+
+   These calls take no handle. Beyond the conventions above:
+   - mk_last_error(NULL) describes a failure (per host thread).
+   - They are asynchronous on `stream`, allocate nothing on the device and
+     keep nothing between calls, so they can be captured into CUDA graphs and
+     called from several host threads; the current device must be the one
+     that owns the stream and the pointers.
+   - Scratch is the caller's: a workspace (DEVICE, 256-byte aligned, at least
+     as large as its query says, contents arbitrary) belongs to one call until
+     that call has completed on its stream. Calls that may overlap, such as
+     two captured graphs replayed at once, need a workspace each.
+   - Arrays marked DEVICE are read when the kernel runs. The host cannot check
+     them, so every value in them has a meaning: starts outside [0, capacity]
+     and counts outside [0, n_tokens] are taken as the nearer bound; a block
+     table entry outside [0, n_blocks) is a page that is not there (its keys
+     are not seen, rows for it are dropped), as is every slot at or behind the
+     capacity. */
+
+/* A cache as the operators see it: the one of mk_create (contiguous:
+   block_table NULL, n_blocks = sequences, block_size = kv_capacity; sequence b
+   is block b) or of mk_create_paged. Layer l's k[l] / v[l]: bf16
+   [n_blocks][n_kv_heads][block_size][head_dim]; slot s of sequence b is row
+   s % block_size of block block_table[b][s / block_size]. Capacity:
+   table_entries * block_size (contiguous: block_size) slots per sequence.
+   head_dim 64 or 128, n_layers 1 to 64, batch 1 to 1024. */
+typedef struct {
+  int n_layers, n_kv_heads, head_dim;
+  int n_blocks, block_size;
+  int batch;                  /* sequences (contiguous: at most n_blocks) */
+  int table_entries;          /* entries per sequence; 0 when contiguous */
+  const int32_t* block_table; /* DEVICE [batch][table_entries]; NULL: contiguous */
+  void* const* k;             /* HOST array of n_layers DEVICE pointers */
+  void* const* v;
+} mk_cache;
+
+/* Element types of activations and logits. */
+#define MK_TYPE_BF16 0
+#define MK_TYPE_FP32 1
+
+/* A tree of drafted tokens: parents (DEVICE int32 [batch][n_tokens], n_tokens
+   at most MK_MAX_TREE) names each node's parent; a value outside
+   [0, node) makes the node a root, which hangs off the context itself. NULL:
+   a chain, each node the parent of the next. counts (DEVICE int32 [batch],
+   NULL: n_tokens everywhere): the nodes sequence b really has; rows of the
+   others are neither read nor written. Node t of sequence b has the cache
+   slot starts[b] + t and the position starts[b] + its depth. */
+#define MK_MAX_TREE 64
+
+/* Rotary positions. Pair i of the first rotary_dim dimensions of a head (the
+   others pass through) turns by position * f_i, f_i = theta^(-2i / rotary_dim)
+   scaled as `scaling` says, and is multiplied by `magnitude`.
+   interleaved 0: pair i is (i, i + rotary_dim / 2), as the decode step has it;
+   1: (2i, 2i + 1). */
+#define MK_ROPE_NONE 0
+#define MK_ROPE_LINEAR 1 /* f / factor */
+#define MK_ROPE_BANDS 2  /* by the turns n = original_length f / (2 pi): below
+                            `low` f / factor, above `high` f, linear in n
+                            between */
+#define MK_ROPE_YARN 3   /* by dimension: f up to the pair that makes `high`
+                            turns over original_length, f / factor from the one
+                            that makes `low`, linear between */
+typedef struct {
+  int head_dim, rotary_dim; /* rotary_dim even, 2 to head_dim */
+  int interleaved, scaling;
+  float theta, factor, low, high; /* theta >= 1, factor >= 1 */
+  int original_length;      /* MK_ROPE_BANDS, MK_ROPE_YARN */
+  float magnitude;          /* 0: 1, or 0.1 ln(factor) + 1 for MK_ROPE_YARN */
+} mk_rope_config;
+
+/* A plan, filled by mk_rope_init and passed by the caller to each call. */
+typedef struct {
+  int head_dim, rotary_dim, interleaved;
+  float magnitude;
+  uint64_t turns[64]; /* f_i / (2 pi) in units of 2^-64 turns */
+} mk_rope;
+
+/* Host only. MK_ERR_INVALID when a member is out of its range. */
+int mk_rope_init(const mk_rope_config* config, mk_rope* out);
+
+/* Rotates the new tokens' queries and keys and appends their k/v rows to
+   layer `layer` of the cache. q, k, v: DEVICE `type`, row b * n_tokens + t at
+   an offset of that many strides (in elements, 16-byte multiples; at least
+   the row): [n_heads][head_dim], [n_kv_heads][head_dim] twice. q_out (row
+   stride q_out_stride) receives the rotated queries and may be q with q's
+   stride; the k/v rows are rounded to bf16 (nearest even) as the decode step
+   does it. The tree is described above; a chain may be any length (a prompt).
+   Errors: MK_ERR_INVALID, MK_ERR_CUDA. */
+int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int batch,
+                   int n_tokens, int n_heads, int type, const void* q, int64_t q_stride,
+                   const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
+                   int64_t q_out_stride, const int32_t* starts, const int32_t* parents,
+                   const int32_t* counts, void* stream);
+
+/* Attention of the tree's nodes over layer `layer` of the cache: node t sees
+   the slots below starts[b], its ancestors' and its own (their rows are in the
+   cache already: mk_rope_append). q, out: DEVICE `type`, rows as above
+   ([n_heads][head_dim]); n_heads a multiple of n_kv_heads, at most 8 query
+   heads per kv-head; n_tokens 1 to MK_MAX_TREE. Softmax of scale * (q . k) in
+   fp32. A row that sees no key is 0; NaN and infinities in rows it does not
+   see do not reach it. Deterministic: the same inputs give the same bits.
+   Errors: MK_ERR_INVALID (also a workspace below the query's size),
+   MK_ERR_CUDA. */
+int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
+                      int type, float scale, const void* q, int64_t q_stride,
+                      const int32_t* starts, const int32_t* parents, const int32_t* counts,
+                      void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                      void* stream);
+/* Bytes of workspace that mk_tree_attention needs for these arguments on the
+   current device (*bytes). */
+int mk_tree_attention_workspace(const mk_cache* cache, int batch, int n_tokens, int n_heads,
+                                int type, size_t* bytes);
+
+/* Greedy acceptance of a drafted tree. Node 0 is each sequence's last token;
+   logits (DEVICE `type`, row b * n_tokens + t of `vocab` values at a stride of
+   logits_stride elements) are those after each node, tokens (DEVICE int32
+   [batch][n_tokens]) the nodes' own. A node's choice is the largest logit (the
+   lowest index among equal ones; NaN is below everything). From node 0 on, the
+   lowest child whose token is the choice is accepted. Outputs, DEVICE int32:
+   choices [batch][n_tokens] (each node's choice; -1 behind counts[b]),
+   path [batch][n_tokens] (the accepted nodes, ascending, node 0 first; -1
+   behind them), accepted [batch] (how many), next [batch] (the choice of the
+   last one: the token to go on with; -1 when counts[b] is 0).
+   Errors: MK_ERR_INVALID, MK_ERR_CUDA. */
+int mk_tree_accept(int batch, int n_tokens, int vocab, int type, const void* logits,
+                   int64_t logits_stride, const int32_t* tokens, const int32_t* parents,
+                   const int32_t* counts, int32_t* choices, int32_t* path, int32_t* accepted,
+                   int32_t* next, void* workspace, size_t workspace_bytes, void* stream);
+int mk_tree_accept_workspace(int batch, int n_tokens, int vocab, size_t* bytes);
+
+/* Moves the accepted rows down behind the context, in every layer, K and V:
+   row starts[b] + i <- row starts[b] + path[b][i] for i < accepted[b] (DEVICE
+   int32 arrays as mk_tree_accept writes them). Entries that do not ascend,
+   or lie outside [i, n_tokens), are skipped. Errors: MK_ERR_INVALID,
+   MK_ERR_CUDA. */
+int mk_cache_compact(const mk_cache* cache, int batch, int n_tokens, const int32_t* starts,
+                     const int32_t* path, const int32_t* accepted, void* stream);
+
+/* One page copied to another: its first `rows` rows (of every kv-head). */
+typedef struct {
+  int32_t src, dst, rows;
+} mk_block_copy;
+
+/* Copies pages in every layer, K and V. copies: HOST, read before the call
+   returns; src, dst in [0, n_blocks), rows in [0, block_size]; no dst may
+   appear twice or be a src (MK_ERR_INVALID before any launch otherwise, also
+   for rows 0). The table members of the cache are not used and may be 0. */
+int mk_cache_copy_blocks(const mk_cache* cache, const mk_block_copy* copies, int n_copies,
+                         void* stream);
+
+/* Page tables of a paged cache, on the host (no CUDA call): which pages each
+   of n_seqs sequences holds, how many hold each page, which are free. The
+   tables are what mk_decode_step_paged takes. Pages are shared by forked
+   sequences; a sequence about to write into a partly filled page that others
+   hold gets a copy of its own, which the caller makes with
+   mk_cache_copy_blocks before the write. The lowest free page is taken first.
+   A failing call changes nothing. Not thread-safe per object. */
+typedef struct mk_pages mk_pages;
+int mk_pages_create(int n_blocks, int block_size, int n_seqs, int kv_capacity, mk_pages** out);
+int mk_pages_destroy(mk_pages* p);
+
+/* Gives sequence seqs[i] room for lengths[i] positions (i in order; a sequence
+   may be named once): new pages when it grows, pages given back when it
+   shrinks (0: all of them). copies receives the copies to make, at most one
+   for each sequence (capacity >= n always suffices), *n_copies their number.
+   MK_ERR_INVALID: a sequence or length out of range, one named twice, capacity
+   too small; MK_ERR_OOM: not enough free pages. */
+int mk_pages_resize(mk_pages* p, int n, const int32_t* seqs, const int32_t* lengths,
+                    mk_block_copy* copies, int capacity, int* n_copies);
+
+/* children[i], which must be empty, becomes a fork of parents[i]: the same
+   length, the same pages. */
+int mk_pages_fork(mk_pages* p, int n, const int32_t* parents, const int32_t* children);
+
+/* Renumbers the pages in use to the lowest ones (in ascending order, each
+   page above them to the lowest free one) and gives the copies that move their
+   contents. MK_ERR_INVALID (with *n_copies the number needed) when capacity is
+   too small. */
+int mk_pages_compact(mk_pages* p, mk_block_copy* copies, int capacity, int* n_copies);
+
+/* Outputs, each optional: tables [n_seqs][ceil(kv_capacity / block_size)] (-1
+   behind a sequence's pages), lengths [n_seqs], the number of free pages. */
+int mk_pages_read(const mk_pages* p, int32_t* tables, int32_t* lengths, int* n_free);
 
 /* ---- decode step without any allocation -------------------------------- */
 
