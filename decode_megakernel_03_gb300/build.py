@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["mk_kernel.cu", "mk_kernel_fixed_a.cu", "mk_kernel_fixed_b.cu", "mk_kernel_fx.cu",
            "mk_kernel_dyn.cu",
            "mk_abi.cu", "mk_sched.cpp",
-           "mk_noalloc.cu", "mk_cache_ops.cu", "mk_tree_attention.cu", "mk_tree_accept.cu",
+           "mk_noalloc.cu", "mk_cache_ops.cu", "mk_tree_attention.cu",
+           "mk_tree_attention_tc.cu", "mk_tree_accept.cu",
            "mk_pages.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]

@@ -1,21 +1,11 @@
 // Attention of a tree of drafted tokens over a KV cache (include/mk.h,
-// mk_tree_attention).
-//
-// For kv-head g of sequence b the rows are (node, query head of the group):
-// row r = t * G + i, i < G = n_heads / n_kv_heads. All rows of a (b, g) read the
-// same keys, so a key tile is fetched once for a tile of rows. The tiles of all
-// (b, g) form one line of work that is cut into equal shares, one per group
-// of blocks, wherever the cuts fall; the lengths are read on the device, so the
-// grid does not depend on them and a captured call stays valid. A share that
-// covers a (b, g) whole writes its rows; shares that cover a part write
-// (o, m, l) to the workspace and a second kernel joins them.
-#include <cuda_runtime.h>
-
+// mk_tree_attention): the entry point, the kernel for few rows (warp-level
+// products) and the kernel that joins shares. The one for many rows is in
+// mk_tree_attention_tc.cu.
 #include <algorithm>
 #include <type_traits>
 
-#include "mk_ops.h"
-#include "mk_ptx.cuh"
+#include "mk_tree_attention.cuh"
 
 namespace mk {
 namespace {
@@ -25,73 +15,6 @@ constexpr int kStages = 3;       // tiles in shared memory
 constexpr int kThreads = 128;    // four warps, each 16 keys of a tile
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxG = 8;
-
-struct AttnParams {
-  CacheView cache;
-  const uint16_t *k, *v;
-  const void* q;
-  void* out;
-  int64_t qs, os;
-  const int32_t *starts, *parents, *counts;
-  int B, T, nh, G;
-  int row_tiles, groups;  // grid = groups x row_tiles, row tiles fastest
-  float scale_log2;       // scale * log2(e)
-  float* part_o;          // [groups][2][row_tiles][RT][D]
-  float* part_ml;         // [groups][2][row_tiles][RT][2]
-};
-
-// ---- the line of work -----------------------------------------------------------
-// Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), their
-// tiles in order.
-
-struct Item {
-  int b, g, t0, nt;       // nt: tiles of the item; t0: the first tile of this share
-  int64_t first;          // number of the item's tile 0 on the line
-};
-
-__device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
-  const int n = clamped(p.counts, b, p.T);
-  if (n == 0) return 0;
-  return min(clamped(p.starts, b, p.cache.capacity) + n, p.cache.capacity);
-}
-
-// Fills prefix[0..B] (tiles of the sequences before b, times n_kv) with one warp.
-__device__ __forceinline__ void work_line(const AttnParams& p, int64_t* prefix) {
-  const int lane = threadIdx.x % 32;
-  int64_t sum = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    int64_t x = b < p.B ? (int64_t)((keys_of(p, b) + kTile - 1) / kTile) * p.cache.n_kv : 0;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
-    }
-    if (b < p.B) prefix[b + 1] = sum + x;
-    sum += __shfl_sync(0xffffffffu, x, 31);
-  }
-  if (lane == 0) prefix[0] = 0;
-  __syncwarp();
-}
-
-// the group whose share holds tile u of a line of W tiles
-__device__ __forceinline__ int group_of(int64_t u, int64_t W, int groups) {
-  return (int)(((u + 1) * groups - 1) / W);
-}
-
-// ---- asynchronous 16-byte copies ---------------------------------------------------
-// (bytes 0: the destination is zeroed)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -162,26 +85,10 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   int64_t u = group * W / p.groups;
   const int64_t u_begin = u, u_end = (int64_t)(group + 1) * W / p.groups;
 
-  while (u < u_end) {
-    // the item of tile u: the last sequence whose prefix is <= u
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (prefix[mid] <= u) lo = mid;
-      else hi = mid;
-    }
-    const int b = lo;
-    const int nt = (int)((prefix[b + 1] - prefix[b]) / p.cache.n_kv);
-    const int g = (int)((u - prefix[b]) / nt);
-    const int64_t item0 = prefix[b] + (int64_t)g * nt;
-    const int k0 = (int)(u - item0);
-    const int n = (int)min((int64_t)(nt - k0), u_end - u);  // tiles of this share
-    const bool begins = u == u_begin;
-    u += n;
-    const int count = clamped(p.counts, b, p.T);
-    const int start = clamped(p.starts, b, p.cache.capacity);
-    const int len = min(start + count, p.cache.capacity);
-    const int rows = count * p.G;
+  Share sh;
+  while (next_share(p, prefix, u_begin, u_end, u, sh)) {
+    const int b = sh.b, g = sh.g, k0 = sh.k0, n = sh.n;
+    const int count = sh.count, start = sh.start, len = sh.len, rows = sh.rows;
     if (rt * RT >= rows) continue;  // no row of this tile is there
 
     // ---- key rows of tile `it` of the share into rowtab, its copies
@@ -261,7 +168,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         const int r = rt * RT + m * 16 + h * 8 + grp;
         const int t = r / p.G;
         seen[m][h] = r < rows ? s_seen[t] : 0;
-        const int64_t off = ((int64_t)b * p.T + t) * p.qs + (g * p.G + r % p.G) * D;
+        const int64_t off = row_offset(p, b, g, r, D, p.qs);
         src[h] = r >= rows ? nullptr
                  : P > 1    ? (const void*)((const float*)p.q + off)
                            : (const void*)((const uint16_t*)p.q + off);
@@ -353,12 +260,23 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         uint32_t kf[4];
         ldsm_x4(kf, ks + r * (D * 2) + ((c ^ (r & 7)) * 16));
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (P == 1) {
+            mma_bf16_16816(s[m][0], qf[0][m][kb], kf[0], kf[1]);
+            mma_bf16_16816(s[m][1], qf[0][m][kb], kf[2], kf[3]);
+          } else {
+            // the matrix unit may truncate as it accumulates: the smallest parts
+            // first, and the sums over the dimensions by rounded adds
+            float x[2][4] = {};
 #pragma unroll
-          for (int q = 0; q < P; ++q) {
-            mma_bf16_16816(s[m][0], qf[q][m][kb], kf[0], kf[1]);
-            mma_bf16_16816(s[m][1], qf[q][m][kb], kf[2], kf[3]);
+            for (int q = P - 1; q >= 0; --q) {
+              mma_bf16_16816(x[0], qf[q][m][kb], kf[0], kf[1]);
+              mma_bf16_16816(x[1], qf[q][m][kb], kf[2], kf[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[m][0][e] += x[0][e], s[m][1][e] += x[1][e];
           }
+        }
       }
       // what is not seen: keys behind the length, pages that are not there,
       // nodes that are no ancestors
@@ -427,12 +345,21 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         uint32_t vf[4];
         ldsm_x4_t(vf, vs + r * (D * 2) + ((c ^ (r & 7)) * 16));
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (P == 1) {
+            mma_bf16_16816(o[m][d], w[0][m], vf[0], vf[1]);
+            mma_bf16_16816(o[m][d + 1], w[0][m], vf[2], vf[3]);
+          } else {
+            float x[2][4] = {};
 #pragma unroll
-          for (int q = 0; q < P; ++q) {
-            mma_bf16_16816(o[m][d], w[q][m], vf[0], vf[1]);
-            mma_bf16_16816(o[m][d + 1], w[q][m], vf[2], vf[3]);
+            for (int q = P - 1; q >= 0; --q) {
+              mma_bf16_16816(x[0], w[q][m], vf[0], vf[1]);
+              mma_bf16_16816(x[1], w[q][m], vf[2], vf[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[m][d][e] += x[0][e], o[m][d + 1][e] += x[1][e];
           }
+        }
       }
       if (odd) {
 #pragma unroll 1
@@ -484,8 +411,8 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
               none ? make_float2(0.f, 0.f) : make_float2(o[m][d][2 * h] * f, o[m][d][2 * h + 1] * f);
       }
     __syncthreads();
-    const bool whole = n == nt;
-    const size_t slot = ((size_t)group * 2 + (begins ? 0 : 1)) * p.row_tiles + rt;
+    const bool whole = n == sh.nt;
+    const size_t slot = part_slot(p, group, sh.begins, rt);
     for (int i = tid; i < RT * (D / 4); i += kThreads) {
       const int r = i / (D / 4), c = i % (D / 4) * 4, row = rt * RT + r;
       if (row >= rows) break;
@@ -502,7 +429,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         const float f = l == 0.f ? 0.f : 1.f / l;  // no key seen: 0
         if (l == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);
         a.x *= f, a.y *= f, a.z *= f, a.w *= f;
-        const int64_t off = ((int64_t)b * p.T + row / p.G) * p.os + (g * p.G + row % p.G) * D + c;
+        const int64_t off = row_offset(p, b, g, row, D, p.os) + c;
         if constexpr (P > 1)
           *reinterpret_cast<float4*>((float*)p.out + off) = a;
         else
@@ -521,7 +448,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
 
 // Joins the shares of the items that were cut: a warp takes one row, each lane
 // D / 32 of its columns; the shares follow one another in the order of the line.
-template <int D, int RT, typename T>
+template <int D, typename T>
 __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ AttnParams p) {
   constexpr int E = D / 32;
   __shared__ int64_t prefix[kMaxSeqs + 1];
@@ -537,14 +464,14 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
   const int64_t item0 = prefix[b] + (int64_t)g * nt;
   const int g0 = group_of(item0, W, p.groups), g1 = group_of(item0 + nt - 1, W, p.groups);
   if (g0 == g1) return;  // written whole
-  const int rt = row / RT, r = row % RT;
+  const int rt = row / p.row_tile, r = row % p.row_tile;
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   for (int s = g0; s <= g1; ++s) {
     const int64_t u0 = s * W / p.groups, u1 = (int64_t)(s + 1) * W / p.groups;
     if (u0 == u1) continue;  // more groups than tiles
-    const size_t at = (((size_t)s * 2 + (u0 < item0 ? 1 : 0)) * p.row_tiles + rt) * RT + r;
+    const size_t at = part_slot(p, s, u0 >= item0, rt) * p.row_tile + r;
     const float ms = p.part_ml[at * 2], ls = p.part_ml[at * 2 + 1];
     if (ls == 0.f) continue;  // no key of this share is seen
     const float now = fmaxf(m, ms), keep = fast_exp2(m - now), f = fast_exp2(ms - now);
@@ -554,7 +481,7 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
     for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p.part_o[at * D + lane * E + e] * f;
   }
   const float f = l == 0.f ? 0.f : 1.f / l;
-  const int64_t off = ((int64_t)b * p.T + row / p.G) * p.os + (g * p.G + row % p.G) * D + lane * E;
+  const int64_t off = row_offset(p, b, g, row, D, p.os) + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
     const float x = l == 0.f ? 0.f : o[e] * f, y = l == 0.f ? 0.f : o[e + 1] * f;
@@ -566,20 +493,36 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
 }
 
 struct Plan {
-  int row_tile, row_tiles, groups;
+  bool tc;  // the kernel for many rows
+  int tile, row_tile, row_tiles, groups;
   size_t o_floats, ml_floats;
 };
 
-// Rows per tile: 32 for bf16 activations with more than 16 rows; fp32 ones keep
-// three parts of every query in registers, which leaves room for 16 rows.
+// Which kernel, and its tiles. Many rows of bf16 activations go to the
+// tensor-memory kernel: one block per SM, two streams of up to 128 rows each
+// (up to 128 rows: two streams over the same rows that take turns at the key
+// tiles). The others go to the warp-level kernel: 32 rows per tile for bf16
+// activations with more than 16 rows; fp32 ones keep three parts of every query
+// in registers, which leaves room for 16.
 Plan plan_of(int T, int G, int D, int type, int n_sm) {
   Plan pl;
-  pl.row_tile = type == MK_TYPE_BF16 && T * G > 16 ? 32 : 16;
-  pl.row_tiles = (T * G + pl.row_tile - 1) / pl.row_tile;
-  pl.groups = std::max(1, kCtasPerSm * n_sm / pl.row_tiles);
-  const size_t rows = (size_t)pl.groups * 2 * pl.row_tiles * pl.row_tile;
-  pl.o_floats = rows * D;
-  pl.ml_floats = rows * 2;
+  const int rows = T * G;
+  pl.tc = type == MK_TYPE_BF16 && rows > 32;
+  if (pl.tc) {
+    pl.tile = 128;
+    pl.row_tiles = (rows + 255) / 256;
+    const int each = (rows + pl.row_tiles - 1) / pl.row_tiles;
+    pl.row_tile = each <= 128 ? 128 : (each + 63) / 64 * 64;
+    pl.groups = std::max(1, n_sm / pl.row_tiles);
+  } else {
+    pl.tile = kTile;
+    pl.row_tile = type == MK_TYPE_BF16 && rows > 16 ? 32 : 16;
+    pl.row_tiles = (rows + pl.row_tile - 1) / pl.row_tile;
+    pl.groups = std::max(1, kCtasPerSm * n_sm / pl.row_tiles);
+  }
+  const size_t slots = (size_t)pl.groups * 2 * pl.row_tiles * pl.row_tile;
+  pl.o_floats = slots * D;
+  pl.ml_floats = slots * 2;
   return pl;
 }
 
@@ -614,7 +557,17 @@ int launch(const AttnParams& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
   if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
   fn<<<p.groups * p.row_tiles, kThreads, Lay::kBytes, st>>>(p);
-  if (int rc = op_cuda(cudaGetLastError(), "mk_tree_attention")) return rc;
+  return op_cuda(cudaGetLastError(), "mk_tree_attention");
+}
+
+template <int D>
+int launch_all(const AttnParams& p, const Plan& pl, int type, cudaStream_t st) {
+  int rc;
+  if (pl.tc) rc = launch_tree_attention_tc(p, D, st);
+  else if (type == MK_TYPE_FP32) rc = launch<D, 1, 3>(p, st);
+  else if (pl.row_tile == 32) rc = launch<D, 2, 1>(p, st);
+  else rc = launch<D, 1, 1>(p, st);
+  if (rc) return rc;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -624,9 +577,8 @@ int launch(const AttnParams& p, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  using T = typename std::conditional<(P > 1), float, uint16_t>::type;
-  return op_cuda(cudaLaunchKernelEx(&cfg, tree_attention_join<D, Lay::RT, T>, p),
-                 "mk_tree_attention");
+  auto* fn = type == MK_TYPE_FP32 ? tree_attention_join<D, float> : tree_attention_join<D, uint16_t>;
+  return op_cuda(cudaLaunchKernelEx(&cfg, fn, p), "mk_tree_attention");
 }
 
 }  // namespace
@@ -676,18 +628,12 @@ int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens,
   p.q = q, p.out = out, p.qs = q_stride, p.os = out_stride;
   p.starts = starts, p.parents = parents, p.counts = counts;
   p.B = batch, p.T = n_tokens, p.nh = n_heads, p.G = n_heads / cache->n_kv_heads;
-  p.row_tiles = pl.row_tiles, p.groups = pl.groups;
+  p.tile = pl.tile, p.row_tile = pl.row_tile, p.row_tiles = pl.row_tiles, p.groups = pl.groups;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + pl.o_floats;
   cudaStream_t st = (cudaStream_t)stream;
-  const bool wide = pl.row_tile == 32;
-  if (cache->head_dim == 64) {
-    if (type == MK_TYPE_FP32) return launch<64, 1, 3>(p, st);
-    return wide ? launch<64, 2, 1>(p, st) : launch<64, 1, 1>(p, st);
-  }
-  if (type == MK_TYPE_FP32) return launch<128, 1, 3>(p, st);
-  return wide ? launch<128, 2, 1>(p, st) : launch<128, 1, 1>(p, st);
+  return cache->head_dim == 64 ? launch_all<64>(p, pl, type, st) : launch_all<128>(p, pl, type, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,131 @@
+// Attention of a tree of drafted tokens (include/mk.h, mk_tree_attention): what its
+// kernels share -- the parameters, the line of work and its shares.
+//
+// For kv-head g of sequence b the rows are (node, query head of the group):
+// row r = t * G + i, i < G = n_heads / n_kv_heads. All rows of a (b, g) read the
+// same keys, so a key tile is fetched once for a tile of rows. The tiles of all
+// (b, g) form one line of work that is cut into equal shares, one per group
+// of blocks, wherever the cuts fall; the lengths are read on the device, so the
+// grid does not depend on them and a captured call stays valid. A share that
+// covers a (b, g) whole writes its rows; shares that cover a part write
+// (o, m, l) to the workspace and a second kernel joins them.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "mk_ops.h"
+#include "mk_ptx.cuh"
+
+namespace mk {
+
+struct AttnParams {
+  CacheView cache;
+  const uint16_t *k, *v;
+  const void* q;
+  void* out;
+  int64_t qs, os;
+  const int32_t *starts, *parents, *counts;
+  int B, T, nh, G;
+  int tile;                    // keys of a tile
+  int row_tile;                // rows of a row tile
+  int row_tiles, groups;       // grid = groups x row_tiles, row tiles fastest
+  float scale_log2;            // scale * log2(e)
+  float* part_o;               // [groups][2][row_tiles][row_tile][D]
+  float* part_ml;              // [groups][2][row_tiles][row_tile][2]: (max, sum)
+};
+
+// ---- the line of work -----------------------------------------------------------
+// Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), their
+// tiles in order.
+
+__device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
+  const int n = clamped(p.counts, b, p.T);
+  if (n == 0) return 0;
+  return min(clamped(p.starts, b, p.cache.capacity) + n, p.cache.capacity);
+}
+
+// Fills prefix[0..B] (tiles of the sequences before b, times n_kv) with one warp.
+__device__ __forceinline__ void work_line(const AttnParams& p, int64_t* prefix) {
+  const int lane = threadIdx.x % 32;
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t x = b < p.B ? (int64_t)((keys_of(p, b) + p.tile - 1) / p.tile) * p.cache.n_kv : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (b < p.B) prefix[b + 1] = sum + x;
+    sum += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) prefix[0] = 0;
+  __syncwarp();
+}
+
+// the group whose share holds tile u of a line of W tiles
+__device__ __forceinline__ int group_of(int64_t u, int64_t W, int groups) {
+  return (int)(((u + 1) * groups - 1) / W);
+}
+
+// A share of the line that lies in one item: tiles [k0, k0 + n) of the nt tiles of
+// kv-head g of sequence b.
+struct Share {
+  int b, g, k0, n, nt;
+  bool begins;  // it begins where the group's part of the line begins
+  int count, start, len, rows;
+};
+
+// The share at tile u, which moves behind it. False at the end of the part.
+__device__ __forceinline__ bool next_share(const AttnParams& p, const int64_t* prefix,
+                                           int64_t u_begin, int64_t u_end, int64_t& u, Share& s) {
+  if (u >= u_end) return false;
+  int lo = 0, hi = p.B;  // the last sequence whose prefix is <= u
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (prefix[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  s.b = lo;
+  s.nt = (int)((prefix[lo + 1] - prefix[lo]) / p.cache.n_kv);
+  s.g = (int)((u - prefix[lo]) / s.nt);
+  s.k0 = (int)(u - prefix[lo] - (int64_t)s.g * s.nt);
+  s.n = (int)min((int64_t)(s.nt - s.k0), u_end - u);
+  s.begins = u == u_begin;
+  u += s.n;
+  s.count = clamped(p.counts, s.b, p.T);
+  s.start = clamped(p.starts, s.b, p.cache.capacity);
+  s.len = min(s.start + s.count, p.cache.capacity);
+  s.rows = s.count * p.G;
+  return true;
+}
+
+// the number of a row tile of a share in the workspace
+__device__ __forceinline__ size_t part_slot(const AttnParams& p, int group, bool begins, int rt) {
+  return ((size_t)group * 2 + (begins ? 0 : 1)) * p.row_tiles + rt;
+}
+
+// offset of a row (of kv-head g of sequence b) in q or out
+__device__ __forceinline__ int64_t row_offset(const AttnParams& p, int b, int g, int row, int D,
+                                              int64_t stride) {
+  return ((int64_t)b * p.T + row / p.G) * stride + (g * p.G + row % p.G) * D;
+}
+
+// ---- asynchronous 16-byte copies ---------------------------------------------------
+// (bytes 0: the destination is zeroed)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Launch of the kernel for many rows (mk_tree_attention_tc.cu).
+int launch_tree_attention_tc(const AttnParams& p, int head_dim, cudaStream_t st);
+
+}  // namespace mk
