@@ -66,7 +66,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   constexpr int RT = Lay::RT, KB = D / 16, NB = D / 8;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t* rowtab = reinterpret_cast<uint32_t*>(smem + Lay::kRing);  // [kStages + 1][kTile]
-  __shared__ int64_t prefix[kMaxSeqs + 1];
+  __shared__ int prefix[kMaxSeqs + 1];
   __shared__ uint64_t s_seen[MK_MAX_TREE];   // node -> the nodes it sees
   __shared__ int s_up[MK_MAX_TREE];
   // non-finite values of the nodes' v rows: bit d % 32 of word d / 32, +inf in
@@ -81,9 +81,9 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   griddep_launch();
   if (warp == 0) work_line(p, prefix);
   __syncthreads();
-  const int64_t W = prefix[p.B];
-  int64_t u = group * W / p.groups;
-  const int64_t u_begin = u, u_end = (int64_t)(group + 1) * W / p.groups;
+  const Cut cut(prefix[p.B], p.groups);
+  const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
+  int u = u_begin;
 
   Share sh;
   while (next_share(p, prefix, u_begin, u_end, u, sh)) {
@@ -446,45 +446,101 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   }
 }
 
-// Joins the shares of the items that were cut: a warp takes one row, each lane
-// D / 32 of its columns; the shares follow one another in the order of the line.
-template <int D, typename T>
+// Joins the shares of the items that were cut. WPR warps take a row (few rows:
+// all four of the block, many: one each), each lane D / 32 of its columns. The
+// lanes read the shares' maxima and sums 32 at a time, so that every share's
+// factor is known before its columns are read; the warps of a row take the
+// shares in turn and add up in shared memory, in a fixed order.
+template <int D, int WPR, typename T>
 __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32;
-  __shared__ int64_t prefix[kMaxSeqs + 1];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int E = D / 32, ROWS = 4 / WPR;
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
+  __shared__ int prefix[kMaxSeqs + 1];
+  __shared__ Vec other[4][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, turn = warp % WPR;
   const int b = blockIdx.y / p.cache.n_kv, g = blockIdx.y % p.cache.n_kv;
   if (warp == 0) work_line(p, prefix);
   __syncthreads();
+  const int row = blockIdx.x * ROWS + warp / WPR;
+  const int nt = (prefix[b + 1] - prefix[b]) / p.cache.n_kv;
+  const int rt = row / p.row_tile, r = row - rt * p.row_tile;
+  bool cut_up = nt > 0 && row < clamped(p.counts, b, p.T) * p.G;
+  int g0 = 0, g1 = 0, item0 = 0;
+  const Cut cut(prefix[p.B], p.groups);
+  if (cut_up) {
+    item0 = prefix[b] + g * nt;
+    g0 = cut.group_of(item0);
+    g1 = cut.group_of(item0 + nt - 1);
+    cut_up = g0 != g1;  // else it was written whole
+  }
   griddep_wait();
-  const int row = blockIdx.x * 4 + warp, count = clamped(p.counts, b, p.T);
-  const int64_t W = prefix[p.B];
-  const int nt = (int)((prefix[b + 1] - prefix[b]) / p.cache.n_kv);
-  if (nt == 0 || row >= count * p.G) return;
-  const int64_t item0 = prefix[b] + (int64_t)g * nt;
-  const int g0 = group_of(item0, W, p.groups), g1 = group_of(item0 + nt - 1, W, p.groups);
-  if (g0 == g1) return;  // written whole
-  const int rt = row / p.row_tile, r = row % p.row_tile;
-  float m = -INFINITY, l = 0.f, o[E];
+  float l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int s = g0; s <= g1; ++s) {
-    const int64_t u0 = s * W / p.groups, u1 = (int64_t)(s + 1) * W / p.groups;
-    if (u0 == u1) continue;  // more groups than tiles
-    const size_t at = part_slot(p, s, u0 >= item0, rt) * p.row_tile + r;
-    const float ms = p.part_ml[at * 2], ls = p.part_ml[at * 2 + 1];
-    if (ls == 0.f) continue;  // no key of this share is seen
-    const float now = fmaxf(m, ms), keep = fast_exp2(m - now), f = fast_exp2(ms - now);
-    m = now;
-    l = l * keep + ls * f;
+  if (cut_up) {
+    // lane i: where share s0 + i keeps the row (-1: no share, or no key seen in
+    // it), its maximum and sum
+    int64_t at;
+    float ms, ls;
+    auto look = [&](int s0) {
+      const int s = s0 + lane;
+      at = -1, ms = -INFINITY, ls = 0.f;
+      if (s <= g1) {
+        const int u0 = cut.begin(s);
+        if (u0 != cut.begin(s + 1)) {  // not one of more groups than tiles
+          const int64_t x = (int64_t)part_slot(p, s, u0 >= item0, rt) * p.row_tile + r;
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + x);
+          if (ml.y != 0.f) at = x, ms = ml.x, ls = ml.y;
+        }
+      }
+    };
+    float m = -INFINITY;
+    for (int s0 = g0; s0 <= g1; s0 += 32) {
+      look(s0);
+      m = fmaxf(m, ms);
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + p.part_o[at * D + lane * E + e] * f;
+    for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    for (int s0 = g0; s0 <= g1; s0 += 32) {
+      if (g1 - g0 >= 32) look(s0);  // else the lanes still have it
+      const float f = at < 0 ? 0.f : fast_exp2(ms - m);
+      l += ls * f;
+      const int n = min(32, g1 - s0 + 1);
+#pragma unroll 4
+      for (int i = turn; i < n; i += WPR) {
+        const int64_t x = __shfl_sync(0xffffffffu, at, i);
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        if (x >= 0) {
+          const Vec v = __ldcg(reinterpret_cast<const Vec*>(p.part_o + x * D) + lane);
+          const float* c = reinterpret_cast<const float*>(&v);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += c[e] * w;
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
   }
-  const float f = l == 0.f ? 0.f : 1.f / l;
+  if constexpr (WPR > 1) {
+    Vec v;
+#pragma unroll
+    for (int e = 0; e < E; ++e) reinterpret_cast<float*>(&v)[e] = o[e];
+    other[warp][lane] = v;
+    __syncthreads();
+    if (turn != 0) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      const Vec x = other[warp + w][lane];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] += reinterpret_cast<const float*>(&x)[e];
+    }
+  }
+  if (!cut_up) return;
+  const float f = 1.f / l;
   const int64_t off = row_offset(p, b, g, row, D, p.os) + lane * E;
 #pragma unroll
   for (int e = 0; e < E; e += 2) {
-    const float x = l == 0.f ? 0.f : o[e] * f, y = l == 0.f ? 0.f : o[e + 1] * f;
+    const float x = l == 0.f ? 0.f : o[e] * f, y = l == 0.f ? 0.f : o[e + 1] * f;  // 0: no key seen
     if constexpr (sizeof(T) == 4)
       *reinterpret_cast<float2*>((float*)p.out + off + e) = make_float2(x, y);
     else
@@ -538,6 +594,8 @@ int check_attention(const mk_cache* cache, int batch, int n_tokens, int n_heads,
   if (n_heads < 1 || n_heads % cache->n_kv_heads || n_heads / cache->n_kv_heads > kMaxG)
     return op_fail(MK_ERR_INVALID,
                    "n_heads must be a multiple of n_kv_heads, at most 8 heads per kv-head");
+  if ((int64_t)batch * cache->n_kv_heads * (view->capacity / kTile + 1) > INT32_MAX)
+    return op_fail(MK_ERR_INVALID, "batch x n_kv_heads x capacity above 2^37");
   return MK_OK;
 }
 
@@ -554,8 +612,8 @@ template <int D, int MT, int P>
 int launch(const AttnParams& p, cudaStream_t st) {
   using Lay = Layout<D, MT, P>;
   auto* fn = tree_attention_kernel<D, MT, P>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
-  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  static std::atomic<uint64_t> ready{0};
+  if (int rc = allow_shared(ready, (const void*)fn, Lay::kBytes)) return rc;
   fn<<<p.groups * p.row_tiles, kThreads, Lay::kBytes, st>>>(p);
   return op_cuda(cudaGetLastError(), "mk_tree_attention");
 }
@@ -572,12 +630,16 @@ int launch_all(const AttnParams& p, const Plan& pl, int type, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.T * p.G + 3) / 4, p.B * p.cache.n_kv);
+  // four warps for a row where that still leaves few blocks per SM
+  const bool few = (int64_t)p.T * p.G * p.B * p.cache.n_kv <= 2048;
+  cfg.gridDim = dim3(few ? p.T * p.G : (p.T * p.G + 3) / 4, p.B * p.cache.n_kv);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto* fn = type == MK_TYPE_FP32 ? tree_attention_join<D, float> : tree_attention_join<D, uint16_t>;
+  auto* fn = type == MK_TYPE_FP32
+                 ? (few ? tree_attention_join<D, 4, float> : tree_attention_join<D, 1, float>)
+                 : (few ? tree_attention_join<D, 4, uint16_t> : tree_attention_join<D, 1, uint16_t>);
   return op_cuda(cudaLaunchKernelEx(&cfg, fn, p), "mk_tree_attention");
 }
 

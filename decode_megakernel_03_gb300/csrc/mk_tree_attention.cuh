@@ -13,6 +13,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "mk_ops.h"
 #include "mk_ptx.cuh"
 
@@ -45,15 +47,16 @@ __device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
 }
 
 // Fills prefix[0..B] (tiles of the sequences before b, times n_kv) with one warp.
-__device__ __forceinline__ void work_line(const AttnParams& p, int64_t* prefix) {
+// (The host makes sure that the line has fewer than 2^31 tiles.)
+__device__ __forceinline__ void work_line(const AttnParams& p, int* prefix) {
   const int lane = threadIdx.x % 32;
-  int64_t sum = 0;
+  int sum = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int64_t x = b < p.B ? (int64_t)((keys_of(p, b) + p.tile - 1) / p.tile) * p.cache.n_kv : 0;
+    int x = b < p.B ? (keys_of(p, b) + p.tile - 1) / p.tile * p.cache.n_kv : 0;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
       if (lane >= d) x += y;
     }
     if (b < p.B) prefix[b + 1] = sum + x;
@@ -63,10 +66,23 @@ __device__ __forceinline__ void work_line(const AttnParams& p, int64_t* prefix) 
   __syncwarp();
 }
 
-// the group whose share holds tile u of a line of W tiles
-__device__ __forceinline__ int group_of(int64_t u, int64_t W, int groups) {
-  return (int)(((u + 1) * groups - 1) / W);
-}
+// The cut of a line of W tiles: group s has the tiles [begin(s), begin(s + 1)),
+// begin(s) = floor(s W / groups) = s q + floor(s r / groups).
+struct Cut {
+  int W, groups, q, r;
+  __device__ __forceinline__ Cut(int W_, int groups_) : W(W_), groups(groups_) {
+    q = W / groups;
+    r = W - q * groups;
+  }
+  __device__ __forceinline__ int begin(int s) const {
+    return s * q + (int)((unsigned)(s * r) / (unsigned)groups);
+  }
+  // the group that has tile u
+  __device__ __forceinline__ int group_of(int u) const {
+    const uint64_t x = (uint64_t)(u + 1) * groups - 1;
+    return x >> 32 ? (int)(x / (unsigned)W) : (int)((unsigned)x / (unsigned)W);
+  }
+};
 
 // A share of the line that lies in one item: tiles [k0, k0 + n) of the nt tiles of
 // kv-head g of sequence b.
@@ -77,8 +93,8 @@ struct Share {
 };
 
 // The share at tile u, which moves behind it. False at the end of the part.
-__device__ __forceinline__ bool next_share(const AttnParams& p, const int64_t* prefix,
-                                           int64_t u_begin, int64_t u_end, int64_t& u, Share& s) {
+__device__ __forceinline__ bool next_share(const AttnParams& p, const int* prefix, int u_begin,
+                                           int u_end, int& u, Share& s) {
   if (u >= u_end) return false;
   int lo = 0, hi = p.B;  // the last sequence whose prefix is <= u
   while (hi - lo > 1) {
@@ -87,10 +103,10 @@ __device__ __forceinline__ bool next_share(const AttnParams& p, const int64_t* p
     else hi = mid;
   }
   s.b = lo;
-  s.nt = (int)((prefix[lo + 1] - prefix[lo]) / p.cache.n_kv);
-  s.g = (int)((u - prefix[lo]) / s.nt);
-  s.k0 = (int)(u - prefix[lo] - (int64_t)s.g * s.nt);
-  s.n = (int)min((int64_t)(s.nt - s.k0), u_end - u);
+  s.nt = (prefix[lo + 1] - prefix[lo]) / p.cache.n_kv;
+  s.g = (u - prefix[lo]) / s.nt;
+  s.k0 = u - prefix[lo] - s.g * s.nt;
+  s.n = min(s.nt - s.k0, u_end - u);
   s.begins = u == u_begin;
   u += s.n;
   s.count = clamped(p.counts, s.b, p.T);
@@ -123,6 +139,20 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Allows a kernel its dynamic shared memory, once on each device (ready: a bit per
+// device; doing it twice does no harm).
+inline int allow_shared(std::atomic<uint64_t>& ready, const void* fn, int bytes) {
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  const uint64_t bit = 1ull << (device & 63);
+  if (device < 64 && (ready.load(std::memory_order_acquire) & bit)) return MK_OK;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  ready.fetch_or(bit, std::memory_order_release);
+  return MK_OK;
 }
 
 // Launch of the kernel for many rows (mk_tree_attention_tc.cu).

@@ -179,9 +179,9 @@ struct Waiter {
 // ---- the loading warps -------------------------------------------------------------
 
 template <int D, bool TWO>
-__device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const int64_t* prefix,
-                                          uint32_t ring, uint8_t* ring_ptr, int64_t u_begin,
-                                          int64_t u_end, int rt) {
+__device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const int* prefix,
+                                          uint32_t ring, uint8_t* ring_ptr, int u_begin,
+                                          int u_end, int rt) {
   using Lay = Layout<D, TWO>;
   constexpr int LEAD = TWO ? 1 : 2;      // K tiles ahead of V
   constexpr int CPR = D / 8, RPW = 32 / CPR;
@@ -189,7 +189,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
   Waiter wait(sm);
   uint32_t buf = 0, round = 0;           // next buffer of the ring, its round
   uint32_t tile_no = 0;                  // K tiles loaded so far
-  int64_t u = u_begin;
+  int u = u_begin;
   Share sh;
   for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
@@ -290,15 +290,15 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
 // ---- the issuing thread ----------------------------------------------------------------
 
 template <int D, bool TWO>
-__device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const int64_t* prefix,
+__device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const int* prefix,
                                          uint32_t q_smem, uint32_t ring, uint32_t tmem,
-                                         int64_t u_begin, int64_t u_end, int rt) {
+                                         int u_begin, int u_end, int rt) {
   using Lay = Layout<D, TWO>;
   constexpr uint32_t kScores = instruction(kKeys, false), kValues = instruction(D, true);
   Waiter wait(sm);
   uint32_t buf = 0, round = 0;
   uint32_t p_uses[2] = {0, 0};
-  int64_t u = u_begin;
+  int u = u_begin;
   Share sh;
   auto advance = [&] {
     tc_commit(&sm.empty[buf]);
@@ -422,9 +422,9 @@ __device__ __forceinline__ uint64_t nodes_seen(const AttnParams& p, int b, int c
 }
 
 template <int D, bool TWO>
-__device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, const int64_t* prefix,
-                                             uint8_t* q_ptr, uint32_t tmem, int64_t u_begin,
-                                             int64_t u_end, int rt, int group) {
+__device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, const int* prefix,
+                                             uint8_t* q_ptr, uint32_t tmem, int u_begin,
+                                             int u_end, int rt, int group) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int stream = warp / 4, r = (warp % 4) * 32 + lane;  // row of the stream's block
   const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
@@ -433,7 +433,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
   const int local = TWO ? stream * block_rows + r : r;     // row of the row tile
   Waiter wait(sm);
   uint32_t s_uses = 0, tile_no = 0;
-  int64_t u = u_begin;
+  int u = u_begin;
   Share sh;
   for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
@@ -630,7 +630,7 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   using Lay = Layout<D, TWO>;
   extern __shared__ uint8_t raw[];
   __shared__ Shared sm;
-  __shared__ int64_t prefix[kMaxSeqs + 1];
+  __shared__ int prefix[kMaxSeqs + 1];
   const int warp = threadIdx.x / 32;
   const int rt = blockIdx.x % p.row_tiles, group = blockIdx.x / p.row_tiles;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -660,8 +660,8 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const int64_t W = prefix[p.B];
-  const int64_t u_begin = group * W / p.groups, u_end = (int64_t)(group + 1) * W / p.groups;
+  const Cut cut(prefix[p.B], p.groups);
+  const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
 
   // 12 warps launched with 168 registers each: 8 x 208 + 4 x 88 is the same sum
   if (warp >= kMmaWarp) {
@@ -685,8 +685,8 @@ template <int D, bool TWO>
 int launch(const AttnParams& p, cudaStream_t st) {
   using Lay = Layout<D, TWO>;
   auto* fn = tree_attention_tc_kernel<D, TWO>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kBytes);
-  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  static std::atomic<uint64_t> ready{0};
+  if (int rc = allow_shared(ready, (const void*)fn, Lay::kBytes)) return rc;
   fn<<<p.groups * p.row_tiles, kThreads, Lay::kBytes, st>>>(p);
   return op_cuda(cudaGetLastError(), "mk_tree_attention");
 }

@@ -11,6 +11,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmk.so")
@@ -475,7 +476,6 @@ class Cache:
     """
 
     def __init__(self, k: list, v: list, block_table=None):
-        import torch
         k, v = list(k), list(v)
         if not k or len(k) != len(v):
             raise _bad("k and v must hold a tensor for each layer")
@@ -490,9 +490,10 @@ class Cache:
         self.device = first.device
         self.batch, entries, ptr = self.n_blocks, 0, None
         if block_table is not None:
-            _ints(block_table, 2, self.device, "block_table")
+            if len(block_table.shape) != 2:
+                raise _bad("block_table must be [batch][entries]")
+            ptr = _ints(block_table, self.device, "block_table", block_table.shape)
             self.batch, entries = map(int, block_table.shape)
-            ptr = block_table.data_ptr()
         self.k, self.v, self.block_table = k, v, block_table
         n = self.n_layers
         self._k = (ctypes.c_void_p * n)(*[t.data_ptr() for t in k])
@@ -501,6 +502,7 @@ class Cache:
                               self.batch, entries, ptr, ctypes.cast(self._k, _vpp),
                               ctypes.cast(self._v, _vpp))
         self.ref = ctypes.byref(self.struct)
+        self.workspaces = {}  # bytes of workspace by call shape
 
 
 class Rope:
@@ -525,44 +527,74 @@ class Rope:
         _check(lib().mk_rope_init(ctypes.byref(cfg), self.ref))
 
 
-def _raw_stream(stream, device) -> int:
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
-        raise _bad("stream and tensors are on different devices")
-    return stream.cuda_stream
+# the current stream's handle without making a Stream object (a few microseconds
+# less per call), where this torch has it
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _ints(t, dims: int, device, what: str, shape=None) -> int:
+class _Call:
+    """The launch context of a call on `device`: its raw stream, the device made
+    current, new tensors that belong to the stream."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise _bad("stream and tensors are on different devices")
+        self.device, self.stream, self.guards = device, stream, None
+        self.raw = _current_raw(device.index) if stream is None else stream.cuda_stream
+
+    def __enter__(self):
+        if self.stream is not None or torch.cuda.current_device() != self.device.index:
+            self.guards = [torch.cuda.device(self.device)]
+            if self.stream is not None:
+                self.guards.append(torch.cuda.stream(self.stream))
+            for g in self.guards:
+                g.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guards:
+            for g in reversed(self.guards):
+                g.__exit__(*exc)
+
+    def new(self, shape, dtype, zero=False):
+        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self.device)
+
+
+def _ints(t, device, what: str, shape):
     """The pointer of an int32 index tensor (contiguous, on `device`)."""
-    import torch
+    if t is None:
+        return None
     if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
         raise _bad(f"{what} must be a contiguous int32 tensor on {device}")
-    if t.dim() != dims or (shape is not None and tuple(t.shape) != shape):
-        raise _bad(f"{what} must have the shape {shape if shape else f'of {dims} dimensions'}")
+    if t.shape != shape:
+        raise _bad(f"{what} has the shape {tuple(t.shape)}, not {shape}")
     return t.data_ptr()
 
 
-def _opt_ints(t, dims, device, what, shape):
-    return None if t is None else _ints(t, dims, device, what, shape)
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_FP32}
 
 
 def _type_of(t, what: str) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return TYPE_BF16
-    if t.dtype == torch.float32:
-        return TYPE_FP32
-    raise _bad(f"{what} must be bfloat16 or float32")
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        raise _bad(f"{what} must be bfloat16 or float32")
+    return kind
+
+
+def _queries(q, cache) -> tuple:
+    """(shape, type, row stride) of q [B][T][nh][D]."""
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != cache.head_dim:
+        raise _bad("q must be [batch][tokens][heads][head_dim], the cache's head_dim")
+    return shape, _type_of(q, "q"), _heads(q, shape, q.dtype, cache.device, "q")
 
 
 def _heads(t, shape, dtype, device, what: str) -> int:
     """The row stride of t [B][T][heads][D]: heads packed, rows evenly spaced."""
-    if t.dtype != dtype or t.device != device or t.dim() != 4:
-        raise _bad(f"{what} must be a {dtype} tensor of 4 dimensions on {device}")
-    if tuple(t.shape) != shape:
-        raise _bad(f"{what} has the shape {tuple(t.shape)}, not {shape}")
+    if t.dtype != dtype or t.device != device or t.shape != shape:
+        raise _bad(f"{what} must be a {dtype} tensor of the shape {tuple(shape)} on {device}, not "
+                   f"{t.dtype} {tuple(t.shape)} on {t.device}")
     b, n, h, d = shape
     sb, sn, sh, sd = t.stride()
     if sd != 1 or (h > 1 and sh != d):
@@ -574,55 +606,28 @@ def _heads(t, shape, dtype, device, what: str) -> int:
     return sn
 
 
-def _on_device(device):
-    """Makes `device` current for the launch when it is not."""
-    import contextlib
-
-    import torch
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=None, counts=None,
                 q_out=None, stream=None):
     """mk_rope_append: q [B][T][nh][D], k, v [B][T][nkv][D] (bf16 or fp32; views
     into a fused projection's rows are fine), starts [B], parents [B][T],
     counts [B] int32, all on the device. Returns the rotated queries (q_out,
     which may be q; else a new tensor, whose rows behind counts are 0)."""
-    import torch
     dev = cache.device
-    if q.dim() != 4:
-        raise _bad("q must be [batch][tokens][heads][head_dim]")
-    b, n, nh, d = q.shape
-    kind, dtype = _type_of(q, "q"), q.dtype
-    if d != cache.head_dim:
-        raise _bad("q's head_dim is not the cache's")
-    kv = (b, n, cache.n_kv_heads, d)
-    qs = _heads(q, (b, n, nh, d), dtype, dev, "q")
+    shape, kind, qs = _queries(q, cache)
+    b, n, nh, d = shape
+    kv, dtype = (b, n, cache.n_kv_heads, d), q.dtype
     ks, vs = _heads(k, kv, dtype, dev, "k"), _heads(v, kv, dtype, dev, "v")
-    sp = _ints(starts, 1, dev, "starts", (b,))
-    pp = _opt_ints(parents, 2, dev, "parents", (b, n))
-    cp = _opt_ints(counts, 1, dev, "counts", (b,))
-    st = _raw_stream(stream, dev)
-    with _on_device(dev):
+    sp = _ints(starts, dev, "starts", (b,))
+    pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
+    with _Call(dev, stream) as call:
         if q_out is None:
-            q_out = _new(torch.empty if counts is None else torch.zeros, (b, n, nh, d), dtype, dev,
-                         stream)
-        os_ = _heads(q_out, (b, n, nh, d), dtype, dev, "q_out")
+            q_out, os_ = call.new(shape, dtype, counts is not None), nh * d
+        else:
+            os_ = _heads(q_out, shape, dtype, dev, "q_out")
         _check(lib().mk_rope_append(rope.ref, cache.ref, layer, b, n, nh, kind, q.data_ptr(), qs,
                                     k.data_ptr(), ks, v.data_ptr(), vs, q_out.data_ptr(), os_, sp,
-                                    pp, cp, st))
+                                    pp, cp, call.raw))
     return q_out
-
-
-def _new(make, shape, dtype, device, stream):
-    """A tensor that belongs to `stream` (None: the current one)."""
-    import torch
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return make(shape, dtype=dtype, device=device)
 
 
 def tree_attention(cache: Cache, layer: int, q, starts, parents=None, counts=None, scale=None,
@@ -631,59 +636,52 @@ def tree_attention(cache: Cache, layer: int, q, starts, parents=None, counts=Non
     cache, whose slots starts[b] + t hold the nodes' rows. scale None:
     1 / sqrt(D). Returns out (given, or new; new rows behind counts are 0). The
     workspace is allocated for the call on its stream."""
-    import torch
     dev = cache.device
-    if q.dim() != 4:
-        raise _bad("q must be [batch][tokens][heads][head_dim]")
-    shape = b, n, nh, d = tuple(q.shape)
-    kind, dtype = _type_of(q, "q"), q.dtype
-    if d != cache.head_dim:
-        raise _bad("q's head_dim is not the cache's")
-    qs = _heads(q, shape, dtype, dev, "q")
-    sp = _ints(starts, 1, dev, "starts", (b,))
-    pp = _opt_ints(parents, 2, dev, "parents", (b, n))
-    cp = _opt_ints(counts, 1, dev, "counts", (b,))
-    st = _raw_stream(stream, dev)
-    with _on_device(dev):
-        size = ctypes.c_size_t()
-        _check(lib().mk_tree_attention_workspace(cache.ref, b, n, nh, kind, ctypes.byref(size)))
-        ws = _new(torch.empty, size.value, torch.uint8, dev, stream)
+    shape, kind, qs = _queries(q, cache)
+    b, n, nh, d = shape
+    sp = _ints(starts, dev, "starts", (b,))
+    pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
+    size = cache.workspaces.get((b, n, nh, kind))
+    with _Call(dev, stream) as call:
+        if size is None:
+            need = ctypes.c_size_t()
+            _check(lib().mk_tree_attention_workspace(cache.ref, b, n, nh, kind, ctypes.byref(need)))
+            size = cache.workspaces[b, n, nh, kind] = need.value
+        ws = call.new(size, torch.uint8)
         if out is None:
-            out = _new(torch.empty if counts is None else torch.zeros, shape, dtype, dev, stream)
-        os_ = _heads(out, shape, dtype, dev, "out")
+            out, os_ = call.new(shape, q.dtype, counts is not None), nh * d
+        else:
+            os_ = _heads(out, shape, q.dtype, dev, "out")
         _check(lib().mk_tree_attention(cache.ref, layer, b, n, nh, kind,
                                        d ** -0.5 if scale is None else scale, q.data_ptr(), qs, sp,
-                                       pp, cp, out.data_ptr(), os_, ws.data_ptr(), size.value, st))
+                                       pp, cp, out.data_ptr(), os_, ws.data_ptr(), size, call.raw))
     return out
 
 
 def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     """mk_tree_accept: logits [B][T][V] (bf16 or fp32), tokens [B][T] int32.
     Returns int32 (choices [B][T], path [B][T], accepted [B], next [B])."""
-    import torch
-    dev = logits.device
-    if not logits.is_cuda or logits.dim() != 3:
+    dev, shape = logits.device, logits.shape
+    if not logits.is_cuda or len(shape) != 3:
         raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
     kind = _type_of(logits, "logits")
-    b, n, vocab = logits.shape
+    b, n, vocab = shape
     sb, sn, sv = logits.stride()
     stride = (sb if b > 1 else vocab) if n == 1 else sn
     if (vocab > 1 and sv != 1) or (n > 1 and b > 1 and sb != n * sn):
         raise _bad("logits: rows must be packed and evenly spaced")
-    tp = _ints(tokens, 2, dev, "tokens", (b, n))
-    pp = _opt_ints(parents, 2, dev, "parents", (b, n))
-    cp = _opt_ints(counts, 1, dev, "counts", (b,))
-    st = _raw_stream(stream, dev)
-    with _on_device(dev):
-        size = ctypes.c_size_t()
-        _check(lib().mk_tree_accept_workspace(b, n, vocab, ctypes.byref(size)))
-        ws = _new(torch.empty, size.value, torch.uint8, dev, stream)
-        choices, path, accepted, last = (_new(torch.empty, s, torch.int32, dev, stream)
-                                         for s in ((b, n), (b, n), (b,), (b,)))
-        _check(lib().mk_tree_accept(b, n, vocab, kind, logits.data_ptr(), stride, tp, pp, cp,
-                                    choices.data_ptr(), path.data_ptr(), accepted.data_ptr(),
-                                    last.data_ptr(), ws.data_ptr(), size.value, st))
-    return choices, path, accepted, last
+    tp = _ints(tokens, dev, "tokens", (b, n))
+    pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
+    need = ctypes.c_size_t()
+    _check(lib().mk_tree_accept_workspace(b, n, vocab, ctypes.byref(need)))
+    with _Call(dev, stream) as call:
+        ws = call.new(need.value, torch.uint8)
+        nodes, seqs = call.new((2, b, n), torch.int32), call.new((2, b), torch.int32)
+        at, to = nodes.data_ptr(), seqs.data_ptr()
+        _check(lib().mk_tree_accept(b, n, vocab, kind, logits.data_ptr(), stride, tp, pp, cp, at,
+                                    at + 4 * b * n, to, to + 4 * b, ws.data_ptr(), need.value,
+                                    call.raw))
+    return (*nodes.unbind(), *seqs.unbind())
 
 
 def cache_compact(cache: Cache, starts, path, accepted, stream=None):
@@ -691,15 +689,13 @@ def cache_compact(cache: Cache, starts, path, accepted, stream=None):
     in every layer; starts [B], path [B][T], accepted [B] as tree_accept gives
     them."""
     dev = cache.device
-    b = starts.shape[0]
-    sp = _ints(starts, 1, dev, "starts")
-    pp = _ints(path, 2, dev, "path")
-    if path.shape[0] != b:
-        raise _bad("path must have a row for each sequence")
-    ap = _ints(accepted, 1, dev, "accepted", (b,))
-    st = _raw_stream(stream, dev)
-    with _on_device(dev):
-        _check(lib().mk_cache_compact(cache.ref, b, path.shape[1], sp, pp, ap, st))
+    if len(path.shape) != 2:
+        raise _bad("path must be [batch][tokens]")
+    b, n = path.shape
+    sp = _ints(starts, dev, "starts", (b,))
+    pp, ap = _ints(path, dev, "path", (b, n)), _ints(accepted, dev, "accepted", (b,))
+    with _Call(dev, stream) as call:
+        _check(lib().mk_cache_compact(cache.ref, b, n, sp, pp, ap, call.raw))
 
 
 def cache_copy_blocks(cache: Cache, copies, stream=None):
@@ -708,9 +704,8 @@ def cache_copy_blocks(cache: Cache, copies, stream=None):
     c = np.ascontiguousarray(copies, dtype=np.int32)
     if c.size and (c.ndim != 2 or c.shape[1] != 3):
         raise _bad("copies must be [n][3]")
-    st = _raw_stream(stream, cache.device)
-    with _on_device(cache.device):
-        _check(lib().mk_cache_copy_blocks(cache.ref, c.ctypes.data, c.size // 3, st))
+    with _Call(cache.device, stream) as call:
+        _check(lib().mk_cache_copy_blocks(cache.ref, c.ctypes.data, c.size // 3, call.raw))
 
 
 class Pages:
