@@ -1,10 +1,10 @@
 // Attention of a tree of drafted tokens (include/mk.h, mk_tree_attention): the
 // kernel for many rows of bf16 activations, on the tensor-memory matrix unit.
 //
-// One block per SM, twelve warps:
+// One block per SM, sixteen warps in warpgroups of four:
 //   warps 0-3, 4-7  softmax of stream 0 and 1: one thread per row
-//   warp 8          one thread issues every product
-//   warps 9-11      load the key and value tiles (128 keys each)
+//   warps 8-11      load the key and value tiles (128 keys each, 32 per warp)
+//   warp 12         one thread issues every product (13-15 idle)
 // With two row blocks (TWO) stream s is the rows of block s, over every tile;
 // with one, both streams take the same rows, stream s the tiles of parity s,
 // and stream 0 joins the two at the end. Either way one stream's softmax runs
@@ -32,11 +32,10 @@ namespace mk {
 namespace {
 
 constexpr int kKeys = 128;          // keys of a tile
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 3;
-constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
-constexpr int kLoadThreads = 32 * kLoadWarps;
+constexpr int kSoftWarps = 8, kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12;
+constexpr int kThreads = 512;
+constexpr int kLoadRows = kKeys / kLoadWarps;  // keys of a tile that a loading warp takes
 constexpr int kMasks = 8;           // tiles whose masks are kept
-constexpr int kTabs = 4;            // tiles whose row numbers are kept
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;       // log2 of how far a weight may exceed 1
 
@@ -98,10 +97,10 @@ __device__ __forceinline__ void tmem_wait_st() {
 
 // Shared-memory operand of 128-byte swizzled rows (64 bf16 each, groups of eight
 // rows 1024 bytes apart). Read by rows (K-major) `lead` is unused; read by
-// columns (MN-major) it is the distance of the next 64 columns.
+// columns (MN-major) it is the distance of the next 64 columns. The address
+// field counts 16-byte units: a place inside the tile is an addition to it.
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         1ull << 46 | 2ull << 61;
+  return (uint64_t)(addr >> 4 | (lead >> 4) << 16) | (uint64_t)(1024 >> 4 | 1u << 14 | 2u << 29) << 32;
 }
 // bf16 operands, fp32 accumulator, M = 128
 __host__ __device__ constexpr uint32_t instruction(int n, bool b_by_columns) {
@@ -123,6 +122,26 @@ __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(what), "r"(add)
       : "memory");
+}
+
+// one thread of a converged warp (the products' operands live in uniform
+// registers: code that a whole warp runs up to this choice computes them there)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+// the largest of three (a NaN loses against a number)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// a += b, lane by lane
+__device__ __forceinline__ void add2(unsigned long long& a, unsigned long long b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
 }
 
 // arrives when this thread's earlier asynchronous copies have landed
@@ -149,7 +168,6 @@ struct Shared {
   uint32_t tmem;
   int failed;                      // a wait ran out
   alignas(16) uint32_t mask[kMasks][4];  // keys of a tile that are there
-  uint32_t tab[kTabs][kKeys];      // row numbers of a tile's keys
   // non-finite values of the nodes' v rows (share parity): +inf in [0], -inf in
   // [1], NaN in both; odd: whether there are any
   uint32_t odd[2];
@@ -178,14 +196,17 @@ struct Waiter {
 
 // ---- the loading warps -------------------------------------------------------------
 
+// Warp w of the four takes the keys 32 w .. 32 w + 31 of every tile: lane i finds
+// the row of key i, the copies take it by a shuffle.
 template <int D, bool TWO>
 __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const int* prefix,
-                                          uint32_t ring, uint8_t* ring_ptr, int u_begin,
-                                          int u_end, int rt) {
+                                          uint32_t ring, uint8_t* ring_ptr, int u_begin, int u_end,
+                                          int rt) {
   using Lay = Layout<D, TWO>;
   constexpr int LEAD = TWO ? 1 : 2;      // K tiles ahead of V
   constexpr int CPR = D / 8, RPW = 32 / CPR;
-  const int lt = threadIdx.x - 32 * kLoadWarp, lw = lt / 32, lane = lt % 32;
+  const int lw = threadIdx.x / 32 - kLoadWarp, lane = threadIdx.x % 32;
+  const int c = lane % CPR, r_first = lw * kLoadRows + lane / CPR;
   Waiter wait(sm);
   uint32_t buf = 0, round = 0;           // next buffer of the ring, its round
   uint32_t tile_no = 0;                  // K tiles loaded so far
@@ -193,34 +214,37 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
   Share sh;
   for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
-    auto row_of = [&](int t, int r) -> uint32_t {
-      const int slot = (sh.k0 + t) * kKeys + r;
-      if (t >= sh.n || r >= kKeys || slot >= sh.len) return kNoRow;
+    auto row_of = [&](int t) -> uint32_t {
+      const int slot = (sh.k0 + t) * kKeys + lw * kLoadRows + lane;
+      if (t >= sh.n || slot >= sh.len) return kNoRow;
       const uint32_t row = cache_row(p.cache, sh.b, slot);
       return row == kNoRow ? row : row + (uint32_t)sh.g * p.cache.block_size;
     };
-    uint32_t r0 = row_of(0, lt), r1 = row_of(0, lt + kLoadThreads);
-    const uint32_t first = tile_no;      // number of the share's tile 0
+    // rows of the tile whose K is next, of the LEAD tiles before it (V is to come)
+    uint32_t next = row_of(0), held[LEAD] = {};
 
-    auto copy = [&](const uint16_t* pool, const uint32_t* tab) {
-      const uint32_t base = ring + buf * Lay::kBuf;
-      const int c = lane % CPR;
-#pragma unroll 4
-      for (int r = lw * RPW + lane / CPR; r < kKeys; r += kLoadWarps * RPW) {
-        const uint32_t row = tab[r];
+    auto copy = [&](const uint16_t* pool, uint32_t rows) {
+      const uint32_t base = ring + buf * Lay::kBuf + (c / 8) * (kKeys * 128);
+#pragma unroll
+      for (int i = 0; i < kLoadRows / RPW; ++i) {
+        const uint32_t row = __shfl_sync(0xffffffffu, rows, i * RPW + lane / CPR);
         const bool there = row != kNoRow;
-        cp_async16(base + (c / 8) * (kKeys * 128) + r * 128 + (((c % 8) ^ (r & 7)) * 16),
+        const int r = r_first + i * RPW;
+        cp_async16(base + r * 128 + (((c % 8) ^ (r & 7)) * 16),
                    pool + (there ? (size_t)row * D + 8 * c : 0), there ? 16 : 0);
       }
     };
     auto advance = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.full[buf]);
       if (++buf == Lay::kBufs) buf = 0, ++round;
     };
 
     for (int j = -LEAD; j < sh.n; ++j) {
       if (j >= 0) {
         wait(&sm.empty[buf], round + 1);
-        copy(p.v, sm.tab[(first + j) % kTabs]);
+        const uint32_t rows = held[0];
+        copy(p.v, rows);
         const int slot0 = (sh.k0 + j) * kKeys;
         if (slot0 + kKeys > sh.start) {
           // nodes in the tile: a value that some rows must not see is not
@@ -228,14 +252,13 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
           // here and added at the end to the rows that see it
           asm volatile("cp.async.wait_all;" ::: "memory");
           if (share >= 2) wait(&sm.done[share & 1], share / 2 - 1);  // its list is free again
-          named_bar(2, kLoadThreads);
-          const uint32_t* tab = sm.tab[(first + j) % kTabs];
-          uint8_t* base = ring_ptr + buf * Lay::kBuf;
-          for (int i = lt; i < kKeys * CPR; i += kLoadThreads) {
-            const int r = i / CPR, c = i % CPR, node = slot0 + r - sh.start;
-            if (node < 0 || node >= sh.count || tab[r] == kNoRow) continue;
-            uint16_t* x = reinterpret_cast<uint16_t*>(base + (c / 8) * (kKeys * 128) + r * 128 +
-                                                      (((c % 8) ^ (r & 7)) * 16));
+          __syncwarp();
+          uint8_t* base = ring_ptr + buf * Lay::kBuf + (c / 8) * (kKeys * 128);
+          for (int i = 0; i < kLoadRows / RPW; ++i) {
+            const uint32_t row = __shfl_sync(0xffffffffu, rows, i * RPW + lane / CPR);
+            const int r = r_first + i * RPW, node = slot0 + r - sh.start;
+            if (node < 0 || node >= sh.count || row == kNoRow) continue;
+            uint16_t* x = reinterpret_cast<uint16_t*>(base + r * 128 + (((c % 8) ^ (r & 7)) * 16));
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint16_t v = x[e];
@@ -255,31 +278,20 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
         } else {
           cp_async_arrive(&sm.full[buf]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.full[buf]);
         advance();
       }
+#pragma unroll
+      for (int i = 0; i + 1 < LEAD; ++i) held[i] = held[i + 1];
       if (const int t = j + LEAD; t < sh.n) {
-        uint32_t* tab = sm.tab[tile_no % kTabs];
-        uint32_t* mask = sm.mask[tile_no % kMasks];
-        tab[lt] = r0;
-        const uint32_t m0 = __ballot_sync(0xffffffffu, r0 != kNoRow);
-        const uint32_t m1 = __ballot_sync(0xffffffffu, r1 != kNoRow);
-        if (lt + kLoadThreads < kKeys) tab[lt + kLoadThreads] = r1;
-        named_bar(2, kLoadThreads);
+        const uint32_t there = __ballot_sync(0xffffffffu, next != kNoRow);
         wait(&sm.empty[buf], round + 1);
-        if (lane == 0) {
-          mask[lw] = m0;
-          if (lw == 0) mask[3] = m1;
-        }
-        copy(p.k, tab);
+        if (lane == 0) sm.mask[tile_no % kMasks][lw] = there;
+        copy(p.k, next);
         cp_async_arrive(&sm.full[buf]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.full[buf]);
         advance();
         ++tile_no;
-        r0 = row_of(t + 1, lt);
-        r1 = row_of(t + 1, lt + kLoadThreads);
+        held[LEAD - 1] = next;
+        next = row_of(t + 1);
       }
     }
     ++share;
@@ -287,12 +299,13 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// ---- the issuing thread ----------------------------------------------------------------
+// ---- the issuing warp ------------------------------------------------------------------
+// The whole warp runs the loops and waits; one elected thread issues.
 
 template <int D, bool TWO>
 __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const int* prefix,
-                                         uint32_t q_smem, uint32_t ring, uint32_t tmem,
-                                         int u_begin, int u_end, int rt) {
+                                         uint32_t q_smem, uint32_t ring, uint32_t tmem, int u_begin,
+                                         int u_end, int rt) {
   using Lay = Layout<D, TWO>;
   constexpr uint32_t kScores = instruction(kKeys, false), kValues = instruction(D, true);
   Waiter wait(sm);
@@ -300,33 +313,43 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
   uint32_t p_uses[2] = {0, 0};
   int u = u_begin;
   Share sh;
-  auto advance = [&] {
-    tc_commit(&sm.empty[buf]);
-    if (++buf == Lay::kBufs) buf = 0, ++round;
-  };
-  auto arrived = [&] {  // the next buffer of the ring is there
-    wait(&sm.full[buf], round);
-    fence_async_smem();
-  };
-  // S of stream s from the K tile in the next buffer
-  auto scores = [&](int s) {
-    const uint32_t k = ring + buf * Lay::kBuf, q = q_smem + (TWO ? s * 128 * D * 2 : 0);
+  // S of stream s from the K tile in buffer `at`; free: it is not needed again
+  auto scores = [&](int s, uint32_t at, bool free) {
+    if (elect_one()) {
+      const uint64_t k = operand(ring + at * Lay::kBuf, 16);
+      const uint64_t q = operand(q_smem + (TWO ? s * 128 * D * 2 : 0), 16);
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const uint32_t at = (i / 4) * (kKeys * 128) + (i % 4) * 32;
-      mma_smem(tmem + s * kKeys, operand(q + at, 16), operand(k + at, 16), kScores, i > 0);
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t step = ((i / 4) * (kKeys * 128) + (i % 4) * 32) / 16;
+        mma_smem(tmem + s * kKeys, q + step, k + step, kScores, i > 0);
+      }
+      tc_commit(&sm.s_full[s]);
+      mbar_arrive(&sm.s_full[s]);  // hands on the tile's mask
+      if (free) tc_commit(&sm.empty[at]);
     }
-    tc_commit(&sm.s_full[s]);
-    mbar_arrive(&sm.s_full[s]);  // hands on the tile's mask
+    __syncwarp();
   };
-  auto values = [&](int s, bool add) {
-    const uint32_t v = ring + buf * Lay::kBuf;
+  // O of stream s from its weights and the V tile in buffer `at`
+  auto values = [&](int s, uint32_t at, bool add, bool free) {
     wait(&sm.p_full[s], p_uses[s]++);
     tc_fence_after();
+    if (elect_one()) {
+      const uint64_t v = operand(ring + at * Lay::kBuf, kKeys * 128);
 #pragma unroll
-    for (int i = 0; i < kKeys / 16; ++i)
-      mma_tmem(tmem + 2 * kKeys + s * D, tmem + s * kKeys + i * 8, operand(v + i * 2048, kKeys * 128),
-               kValues, add || i > 0);
+      for (int i = 0; i < kKeys / 16; ++i)
+        mma_tmem(tmem + 2 * kKeys + s * D, tmem + s * kKeys + i * 8, v + i * (2048 / 16), kValues,
+                 i > 0 ? 1u : add);
+      if (free) tc_commit(&sm.empty[at]);
+    }
+    __syncwarp();
+  };
+  // waits for the next buffer of the ring and moves behind it
+  auto take = [&]() -> uint32_t {
+    wait(&sm.full[buf], round);
+    fence_async_smem();
+    const uint32_t at = buf;
+    if (++buf == Lay::kBufs) buf = 0, ++round;
+    return at;
   };
   for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
@@ -334,47 +357,33 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
     fence_async_smem();
     tc_fence_after();
     if constexpr (TWO) {
-      arrived();
-      scores(0);
-      scores(1);
-      advance();
+      uint32_t at = take();
+      scores(0, at, false);
+      scores(1, at, true);
       for (int j = 0; j < sh.n; ++j) {
-        arrived();  // V of tile j; the K behind it is waited for below
-        const uint32_t v_buf = buf, v_round = round;
-        uint32_t k_buf = buf + 1, k_round = round;
-        if (k_buf == Lay::kBufs) k_buf = 0, ++k_round;
-        for (int s = 0; s < 2; ++s) {
-          buf = v_buf, round = v_round;
-          values(s, j > 0);
-          if (s == 1) tc_commit(&sm.empty[v_buf]);
-          buf = k_buf, round = k_round;
-          if (j + 1 < sh.n) {
-            if (s == 0) arrived();
-            scores(s);
-          }
+        const bool more = j + 1 < sh.n;
+        const uint32_t v_at = take();
+        values(0, v_at, j > 0, false);
+        if (more) {
+          at = take();
+          scores(0, at, false);
         }
-        if (j + 1 < sh.n) advance();
+        values(1, v_at, j > 0, true);
+        if (more) scores(1, at, true);
       }
     } else {
-      for (int s = 0; s < 2 && s < sh.n; ++s) {
-        arrived();
-        scores(s);
-        advance();
-      }
+      for (int s = 0; s < 2 && s < sh.n; ++s) scores(s, take(), true);
       for (int j = 0; j < sh.n; ++j) {
         const int s = j & 1;
-        arrived();
-        values(s, j >= 2);
-        advance();
-        if (j + 2 < sh.n) {
-          arrived();
-          scores(s);
-          advance();
-        }
+        values(s, take(), j >= 2, true);
+        if (j + 2 < sh.n) scores(s, take(), true);
       }
     }
-    tc_commit(&sm.o_full);
-    mbar_arrive(&sm.o_full);
+    if (elect_one()) {
+      tc_commit(&sm.o_full);
+      mbar_arrive(&sm.o_full);
+    }
+    __syncwarp();
     ++share;
   }
 }
@@ -463,11 +472,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
       if (warp_live) {
         uint32_t x[kKeys];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_load32(t_s + 32 * c, x + 32 * c);
+        for (int h = 0; h < 4; ++h) tmem_load32(t_s + 32 * h, x + 32 * h);
         const uint4 there = *reinterpret_cast<const uint4*>(sm.mask[(tile_no + j) % kMasks]);
         const int off = sh.start - (sh.k0 + j) * kKeys;  // first node's place in the tile
-        tmem_wait_ld();
-        if ((there.x & there.y & there.z & there.w) != 0xffffffffu || off < kKeys) {
+        const bool some = (there.x & there.y & there.z & there.w) != 0xffffffffu || off < kKeys;
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        if (some) {
           // context keys below `off`, then the nodes that the row sees
           uint64_t lo, hi;
           if (off >= 128) lo = hi = ~0ull;
@@ -481,26 +491,31 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
             lo = off > -64 ? seen >> -off : 0;
             hi = 0;
           }
-          const uint32_t see[4] = {(uint32_t)lo & there.x, (uint32_t)(lo >> 32) & there.y,
-                                   (uint32_t)hi & there.z, (uint32_t)(hi >> 32) & there.w};
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (!(see[c / 32] >> (c % 32) & 1)) x[c] = 0xff800000u;  // -inf
+          see[0] = (uint32_t)lo & there.x, see[1] = (uint32_t)(lo >> 32) & there.y;
+          see[2] = (uint32_t)hi & there.z, see[3] = (uint32_t)(hi >> 32) & there.w;
         }
-        float top = -INFINITY;
+        tmem_wait_ld();
+        if (some) {
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) top = fmaxf(top, __uint_as_float(x[c]));
-        top *= p.scale_log2;
+          for (int e = 0; e < kKeys; ++e)
+            if (!(see[e / 32] >> (e % 32) & 1)) x[e] = 0xff800000u;  // -inf
+        }
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < kKeys; e += 8)
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            tops[h] = max3(tops[h], __uint_as_float(x[e + 2 * h]), __uint_as_float(x[e + 2 * h + 1]));
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.scale_log2;
         float keep = 1.f;
         if (top > m + kSlack || m == -INFINITY) {
-          keep = fast_exp2(m - top);  // 0 at the first key
-          if (m == -INFINITY) keep = 0.f;
+          keep = m == -INFINITY ? 0.f : fast_exp2(m - top);  // 0 at the first key
           m = top;
           l *= keep;
         }
         const int before = TWO ? j : j / 2;  // tiles already in O
         if (before > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             tmem_load32(t_o + c, o);
@@ -511,19 +526,27 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
           }
         }
         const float from = m == -INFINITY ? 0.f : -m;
+        const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2), from2 = pack2(from, from);
+        unsigned long long sums[2] = {0, 0};
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t w[32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float a = fast_exp2(fmaf(__uint_as_float(x[64 * h + 2 * c]), p.scale_log2, from));
-            const float b = fast_exp2(fmaf(__uint_as_float(x[64 * h + 2 * c + 1]), p.scale_log2, from));
-            l += a + b;
-            w[c] = bf16x2_rn(a, b);
+          for (int e = 0; e < 32; ++e) {
+            unsigned long long z = from2;
+            ffma2(z, pack2(__uint_as_float(x[64 * h + 2 * e]), __uint_as_float(x[64 * h + 2 * e + 1])), scale2);
+            float2 a = unpack2(z);
+            a.x = fast_exp2(a.x);
+            a.y = fast_exp2(a.y);
+            add2(sums[e % 2], pack2(a.x, a.y));
+            w[e] = bf16x2_rn(a.x, a.y);
           }
           tmem_store32(t_s + 32 * h, w);
         }
+        add2(sums[0], sums[1]);
+        const float2 sum = unpack2(sums[0]);
+        l += sum.x + sum.y;
         tmem_wait_st();
       }
       tc_fence_before();
@@ -640,7 +663,7 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   if (warp == 0) work_line(p, prefix);
   if (warp == 1 && threadIdx.x % 32 == 0) {
     for (int i = 0; i < Lay::kBufs; ++i) {
-      mbar_init(&sm.full[i], kLoadThreads + kLoadWarps);
+      mbar_init(&sm.full[i], 32 * kLoadWarps + kLoadWarps);
       mbar_init(&sm.empty[i], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -663,17 +686,17 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   const Cut cut(prefix[p.B], p.groups);
   const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
 
-  // 12 warps launched with 168 registers each: 8 x 208 + 4 x 88 is the same sum
-  if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp >= kLoadWarp)
-      load_role<D, TWO>(p, sm, prefix, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
-    else if (threadIdx.x % 32 == 0)
-      mma_role<D, TWO>(p, sm, prefix, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
-    __syncwarp();
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  // 16 warps launched with 128 registers each: 8 x 200 + 8 x 56 is the same sum
+  if (warp < kSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     softmax_role<D, TWO>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
+  } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    load_role<D, TWO>(p, sm, prefix, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == kMmaWarp)
+      mma_role<D, TWO>(p, sm, prefix, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
   }
   tc_fence_before();
   __syncthreads();
