@@ -162,7 +162,8 @@ struct Layout {
 
 struct Shared {
   uint64_t full[8], empty[8];
-  uint64_t s_full[2], p_full[2];   // a stream's scores / weights are in tensor memory
+  uint64_t s_full[2];              // a stream's scores are in tensor memory
+  uint64_t p_full[2][2];           // the weights of a stream's first, last 64 keys are
   uint64_t q_full, o_full;         // a share's queries are loaded / its products done
   uint64_t done[2];                // a share (by parity) is written
   uint32_t tmem;
@@ -225,13 +226,23 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
 
     auto copy = [&](const uint16_t* pool, uint32_t rows) {
       const uint32_t base = ring + buf * Lay::kBuf + (c / 8) * (kKeys * 128);
+      const uint16_t* from = pool + 8 * c;
+      if (__all_sync(0xffffffffu, rows != kNoRow)) {
 #pragma unroll
-      for (int i = 0; i < kLoadRows / RPW; ++i) {
-        const uint32_t row = __shfl_sync(0xffffffffu, rows, i * RPW + lane / CPR);
-        const bool there = row != kNoRow;
-        const int r = r_first + i * RPW;
-        cp_async16(base + r * 128 + (((c % 8) ^ (r & 7)) * 16),
-                   pool + (there ? (size_t)row * D + 8 * c : 0), there ? 16 : 0);
+        for (int i = 0; i < kLoadRows / RPW; ++i) {
+          const uint32_t row = __shfl_sync(0xffffffffu, rows, i * RPW + lane / CPR);
+          const int r = r_first + i * RPW;
+          cp_async16(base + r * 128 + (((c % 8) ^ (r & 7)) * 16), from + (size_t)row * D);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kLoadRows / RPW; ++i) {
+          const uint32_t row = __shfl_sync(0xffffffffu, rows, i * RPW + lane / CPR);
+          const bool there = row != kNoRow;
+          const int r = r_first + i * RPW;
+          cp_async16(base + r * 128 + (((c % 8) ^ (r & 7)) * 16),
+                     from + (there ? (size_t)row * D : 0), there ? 16 : 0);
+        }
       }
     };
     auto advance = [&] {
@@ -331,17 +342,21 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
   };
   // O of stream s from its weights and the V tile in buffer `at`
   auto values = [&](int s, uint32_t at, bool add, bool free) {
-    wait(&sm.p_full[s], p_uses[s]++);
-    tc_fence_after();
-    if (elect_one()) {
-      const uint64_t v = operand(ring + at * Lay::kBuf, kKeys * 128);
 #pragma unroll
-      for (int i = 0; i < kKeys / 16; ++i)
-        mma_tmem(tmem + 2 * kKeys + s * D, tmem + s * kKeys + i * 8, v + i * (2048 / 16), kValues,
-                 i > 0 ? 1u : add);
-      if (free) tc_commit(&sm.empty[at]);
+    for (int h = 0; h < 2; ++h) {
+      wait(&sm.p_full[s][h], p_uses[s]);
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t v = operand(ring + at * Lay::kBuf, kKeys * 128);
+#pragma unroll
+        for (int i = 4 * h; i < 4 * h + 4; ++i)
+          mma_tmem(tmem + 2 * kKeys + s * D, tmem + s * kKeys + i * 8, v + i * (2048 / 16), kValues,
+                   i > 0 ? 1u : add);
+        if (h == 1 && free) tc_commit(&sm.empty[at]);
+      }
+      __syncwarp();
     }
-    __syncwarp();
+    ++p_uses[s];
   };
   // waits for the next buffer of the ring and moves behind it
   auto take = [&]() -> uint32_t {
@@ -543,15 +558,23 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
             w[e] = bf16x2_rn(a.x, a.y);
           }
           tmem_store32(t_s + 32 * h, w);
+          if (h == 0) {  // the products of the first half need not wait for the second
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.p_full[stream][0]);
+          }
         }
         add2(sums[0], sums[1]);
         const float2 sum = unpack2(sums[0]);
         l += sum.x + sum.y;
         tmem_wait_st();
+      } else if (lane == 0) {
+        mbar_arrive(&sm.p_full[stream][0]);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[stream]);
+      if (lane == 0) mbar_arrive(&sm.p_full[stream][1]);
     }
     tile_no += sh.n;
 
@@ -582,7 +605,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
       const float scale = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       const uint32_t odd = sm.odd[share & 1];
       const size_t slot = part_slot(p, group, sh.begins, rt) * p.row_tile + local;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32], o1[32];
         tmem_load32(t_o + c, o);
@@ -668,7 +691,8 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sm.s_full[s], 2);
-      mbar_init(&sm.p_full[s], 4);
+      mbar_init(&sm.p_full[s][0], 4);
+      mbar_init(&sm.p_full[s][1], 4);
       mbar_init(&sm.done[s], kSoftWarps);
       sm.odd[s] = 0;
     }
@@ -686,12 +710,15 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   const Cut cut(prefix[p.B], p.groups);
   const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
 
-  // 16 warps launched with 128 registers each: 8 x 200 + 8 x 56 is the same sum
+  // Registers: 16 warps launched with 128 each, 8 x 184 + 4 x 88 + 4 x 56 is the
+  // same sum. A row's thread holds a tile's 128 scores; the loading warps need
+  // room for the addresses of the copies in flight (56 registers: 105 cycles a
+  // copy, because each waited for the last one's operands to be read).
   if (warp < kSoftWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     softmax_role<D, TWO>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     load_role<D, TWO>(p, sm, prefix, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
