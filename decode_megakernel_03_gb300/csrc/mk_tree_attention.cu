@@ -27,21 +27,6 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr));
 }
 
-// P bf16 parts of a pair whose sum is the value to 2^-8P of it, each part the
-// rounded rest of the ones before (an infinite part has no rest).
-template <int P>
-__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
-#pragma unroll
-  for (int i = 0; i < P; ++i) {
-    part[i] = bf16x2_rn(a, b);
-    if (i + 1 < P) {
-      const float ha = bf_lo(part[i]), hb = bf_hi(part[i]);
-      a = isinf(ha) ? 0.f : a - ha;
-      b = isinf(hb) ? 0.f : b - hb;
-    }
-  }
-}
-
 // ---- the kernel ------------------------------------------------------------------------
 // MT m16 row blocks per row tile; P = 1: bf16 activations; P = 3: fp32 ones,
 // queries and weights as three bf16 parts (2^-24 of the value: fp32's own
@@ -563,8 +548,13 @@ struct Plan {
 Plan plan_of(int T, int G, int D, int type, int n_sm) {
   Plan pl;
   const int rows = T * G;
-  pl.tc = type == MK_TYPE_BF16 && rows > 32;
-  if (pl.tc) {
+  pl.tc = rows > 16 || type == MK_TYPE_FP32;
+  if (pl.tc && type == MK_TYPE_FP32) {
+    pl.tile = 128;
+    pl.row_tile = 128;
+    pl.row_tiles = (rows + 127) / 128;
+    pl.groups = std::max(1, n_sm / pl.row_tiles);
+  } else if (pl.tc) {
     pl.tile = 128;
     pl.row_tiles = (rows + 255) / 256;
     const int each = (rows + pl.row_tiles - 1) / pl.row_tiles;
@@ -621,7 +611,7 @@ int launch(const AttnParams& p, cudaStream_t st) {
 template <int D>
 int launch_all(const AttnParams& p, const Plan& pl, int type, cudaStream_t st) {
   int rc;
-  if (pl.tc) rc = launch_tree_attention_tc(p, D, st);
+  if (pl.tc) rc = launch_tree_attention_tc(p, D, type, st);
   else if (type == MK_TYPE_FP32) rc = launch<D, 1, 3>(p, st);
   else if (pl.row_tile == 32) rc = launch<D, 2, 1>(p, st);
   else rc = launch<D, 1, 1>(p, st);

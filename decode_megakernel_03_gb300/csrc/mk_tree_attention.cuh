@@ -144,6 +144,21 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// P bf16 parts of a pair whose sum is the value to 2^-8P of it, each part the
+// rounded rest of the ones before (an infinite part has no rest).
+template <int P>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    part[i] = bf16x2_rn(a, b);
+    if (i + 1 < P) {
+      const float ha = bf_lo(part[i]), hb = bf_hi(part[i]);
+      a = isinf(ha) ? 0.f : a - ha;
+      b = isinf(hb) ? 0.f : b - hb;
+    }
+  }
+}
+
 // Allows a kernel its dynamic shared memory, once on each device (ready: a bit per
 // device; doing it twice does no harm).
 inline int allow_shared(std::atomic<uint64_t>& ready, const void* fn, int bytes) {
@@ -159,6 +174,6 @@ inline int allow_shared(std::atomic<uint64_t>& ready, const void* fn, int bytes)
 }
 
 // Launch of the kernel for many rows (mk_tree_attention_tc.cu).
-int launch_tree_attention_tc(const AttnParams& p, int head_dim, cudaStream_t st);
+int launch_tree_attention_tc(const AttnParams& p, int head_dim, int type, cudaStream_t st);
 
 }  // namespace mk

@@ -2,21 +2,28 @@
 // kernel for many rows of bf16 activations, on the tensor-memory matrix unit.
 //
 // One block per SM, sixteen warps in warpgroups of four:
-//   warps 0-3, 4-7  softmax of stream 0 and 1: one thread per row
+//   warps 0-3, 4-7  softmax of stream 0 and 1, one thread per row; fp32: of
+//                   the halves of the rows
 //   warps 8-11      load the key and value tiles (128 keys each, 32 per warp)
 //   warp 12         one thread issues every product (13-15 idle)
-// With two row blocks (TWO) stream s is the rows of block s, over every tile;
-// with one, both streams take the same rows, stream s the tiles of parity s,
-// and stream 0 joins the two at the end. Either way one stream's softmax runs
-// while the matrix unit works for the other.
+// bf16 activations. With two row blocks stream s is the rows of block s, over
+// every tile; with one, both streams take the same rows, stream s the tiles of
+// parity s, and stream 0 joins the two at the end. Either way one stream's
+// softmax runs while the matrix unit works for the other. Per stream and tile:
+// S = Q K^T (128 x 128, fp32, tensor memory); the row's thread reads it, masks
+// it, and writes the weights p = 2^(s - m) back as bf16 over S; O += P V (128 x D,
+// fp32, tensor memory). The reference m of a row follows its maximum only when
+// that exceeds it by 2^8 (or at the first key), so O is almost never rescaled;
+// the sum of the weights is kept in fp32 from the unrounded weights. The
+// weights' rounding to bf16 (relative 2^-8) is the size of the output's own.
 //
-// Per stream and tile: S = Q K^T (128 x 128, fp32, tensor memory); the row's
-// thread reads it, masks it, and writes the weights p = 2^(s - m) back as bf16
-// over S; O += P V (128 x D, fp32, tensor memory). The reference m of a row
-// follows its maximum only when that exceeds it by 2^8 (or at the first key), so
-// O is almost never rescaled; the sum of the weights is kept in fp32 from the
-// unrounded weights. The weights' rounding to bf16 (relative 2^-8) is the
-// size of the output's own.
+// fp32 activations. Queries and weights go in as three bf16 parts (2^-24 of the
+// value), each product runs once per part. The matrix unit truncates as it
+// accumulates, which over a long context costs more than fp32's own rounding, so
+// it sums one tile only (two score buffers, one product) and the rows' threads
+// add the tiles up in registers. (Accumulated in tensor memory the error against
+// 64 bits was 2.5e-6 on 10 thousand keys, twice that of a plain fp32
+// computation.)
 //
 // K and V tiles go through a ring of 16 or 32 KB buffers in the order the
 // products use them, with 16-byte asynchronous copies, so that any page size,
@@ -31,10 +38,9 @@
 namespace mk {
 namespace {
 
-constexpr int kKeys = 128;          // keys of a tile
 constexpr int kSoftWarps = 8, kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12;
 constexpr int kThreads = 512;
-constexpr int kLoadRows = kKeys / kLoadWarps;  // keys of a tile that a loading warp takes
+
 constexpr int kMasks = 8;           // tiles whose masks are kept
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kSlack = 8.f;       // log2 of how far a weight may exceed 1
@@ -86,6 +92,14 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
       "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -152,11 +166,23 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-template <int D, bool TWO>
+// Kinds of call: bf16 with one or two row blocks, fp32.
+enum { kOne, kTwo, kExact };
+
+constexpr int kKeys = 128;  // keys of a tile
+
+// Columns of tensor memory (512): kOne, kTwo: scores (weights over them) of stream
+// s at 128 s, its output at 256 + D s. kExact: scores of tile parity s, the three
+// parts of the weights over them, at 192 s, a tile's product at 384.
+template <int D, int KIND>
 struct Layout {
-  static constexpr int kBuf = kKeys * D * 2;            // a K or V tile
-  static constexpr int kBufs = D == 64 ? 8 : TWO ? 4 : 5;
-  static constexpr int kQ = (TWO ? 2 : 1) * 128 * D * 2;
+  static constexpr bool TWO = KIND == kTwo;
+  static constexpr int PARTS = KIND == kExact ? 3 : 1;
+  static constexpr int kScoreStep = KIND == kExact ? 192 : 128;
+  static constexpr int kOut = 2 * kScoreStep;
+  static constexpr int kBuf = kKeys * D * 2;  // a K or V tile
+  static constexpr int kBufs = D == 64 ? 8 : TWO ? 4 : KIND == kOne ? 5 : 3;
+  static constexpr int kQ = (TWO ? 2 : PARTS) * 128 * D * 2;
   static constexpr int kBytes = kQ + kBufs * kBuf + 1024;  // 1024: alignment of the base
 };
 
@@ -173,7 +199,11 @@ struct Shared {
   // [1], NaN in both; odd: whether there are any
   uint32_t odd[2];
   uint32_t odd_at[2][MK_MAX_TREE][2][4];
-  float ml[128][2];                // stream 1's (m, l), one row block
+  float ml[128][2];                // kOne: stream 1's (m, l)
+  // kExact: a tile's product is in tensor memory / has been read; the halves'
+  // maxima (by tile parity) and sums
+  uint64_t t_full, t_free;
+  float top[2][2][128], sum[2][128];
 };
 
 // Waits with an end: a thread whose wait ran out does not wait again (its
@@ -197,15 +227,17 @@ struct Waiter {
 
 // ---- the loading warps -------------------------------------------------------------
 
-// Warp w of the four takes the keys 32 w .. 32 w + 31 of every tile: lane i finds
-// the row of key i, the copies take it by a shuffle.
-template <int D, bool TWO>
+// Warp w of the four takes a quarter of every tile's keys: lane i finds the row of
+// the quarter's key i, the copies take it by a shuffle.
+template <int D, int KIND>
 __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const int* prefix,
                                           uint32_t ring, uint8_t* ring_ptr, int u_begin, int u_end,
                                           int rt) {
-  using Lay = Layout<D, TWO>;
+  using Lay = Layout<D, KIND>;
+  constexpr bool TWO = Lay::TWO;
   constexpr int LEAD = TWO ? 1 : 2;      // K tiles ahead of V
   constexpr int CPR = D / 8, RPW = 32 / CPR;
+  constexpr int kLoadRows = kKeys / kLoadWarps;  // keys of a tile that a warp takes
   const int lw = threadIdx.x / 32 - kLoadWarp, lane = threadIdx.x % 32;
   const int c = lane % CPR, r_first = lw * kLoadRows + lane / CPR;
   Waiter wait(sm);
@@ -313,15 +345,17 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
 // ---- the issuing warp ------------------------------------------------------------------
 // The whole warp runs the loops and waits; one elected thread issues.
 
-template <int D, bool TWO>
+template <int D, int KIND>
 __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const int* prefix,
                                          uint32_t q_smem, uint32_t ring, uint32_t tmem, int u_begin,
                                          int u_end, int rt) {
-  using Lay = Layout<D, TWO>;
+  using Lay = Layout<D, KIND>;
+  constexpr bool TWO = Lay::TWO;
   constexpr uint32_t kScores = instruction(kKeys, false), kValues = instruction(D, true);
   Waiter wait(sm);
   uint32_t buf = 0, round = 0;
   uint32_t p_uses[2] = {0, 0};
+  uint32_t t_uses = 0;
   int u = u_begin;
   Share sh;
   // S of stream s from the K tile in buffer `at`; free: it is not needed again
@@ -330,29 +364,43 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
       const uint64_t k = operand(ring + at * Lay::kBuf, 16);
       const uint64_t q = operand(q_smem + (TWO ? s * 128 * D * 2 : 0), 16);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t step = ((i / 4) * (kKeys * 128) + (i % 4) * 32) / 16;
-        mma_smem(tmem + s * kKeys, q + step, k + step, kScores, i > 0);
-      }
+      for (int part = Lay::PARTS - 1; part >= 0; --part)  // the smallest part first
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          mma_smem(tmem + s * Lay::kScoreStep,
+                   q + (part * 128 * D * 2 + (i / 4) * (128 * 128) + (i % 4) * 32) / 16,
+                   k + ((i / 4) * (kKeys * 128) + (i % 4) * 32) / 16, kScores,
+                   part < Lay::PARTS - 1 || i > 0);
       tc_commit(&sm.s_full[s]);
       mbar_arrive(&sm.s_full[s]);  // hands on the tile's mask
       if (free) tc_commit(&sm.empty[at]);
     }
     __syncwarp();
   };
-  // O of stream s from its weights and the V tile in buffer `at`
+  // Weights of stream (kExact: tile parity) s times the V tile in buffer `at`: into
+  // the stream's output (add: to what is there), kExact: into the tile's product
   auto values = [&](int s, uint32_t at, bool add, bool free) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       wait(&sm.p_full[s][h], p_uses[s]);
+      if (KIND == kExact && h == 0) wait(&sm.t_free, t_uses++ + 1);
       tc_fence_after();
       if (elect_one()) {
         const uint64_t v = operand(ring + at * Lay::kBuf, kKeys * 128);
 #pragma unroll
-        for (int i = 4 * h; i < 4 * h + 4; ++i)
-          mma_tmem(tmem + 2 * kKeys + s * D, tmem + s * kKeys + i * 8, v + i * (2048 / 16), kValues,
-                   i > 0 ? 1u : add);
-        if (h == 1 && free) tc_commit(&sm.empty[at]);
+        for (int part = Lay::PARTS - 1; part >= 0; --part)
+#pragma unroll
+          for (int i = 4 * h; i < 4 * h + 4; ++i)
+            mma_tmem(tmem + Lay::kOut + (KIND == kExact ? 0 : s * D),
+                     tmem + s * Lay::kScoreStep + part * 64 + i * 8, v + i * (2048 / 16), kValues,
+                     h > 0 || part < Lay::PARTS - 1 || i > 0 ? 1u : add);
+        if (h == 1) {
+          if (free) tc_commit(&sm.empty[at]);
+          if (KIND == kExact) {
+            tc_commit(&sm.t_full);
+            mbar_arrive(&sm.t_full);  // hands on the tile's factors and odd values
+          }
+        }
       }
       __syncwarp();
     }
@@ -390,11 +438,11 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
       for (int s = 0; s < 2 && s < sh.n; ++s) scores(s, take(), true);
       for (int j = 0; j < sh.n; ++j) {
         const int s = j & 1;
-        values(s, take(), j >= 2, true);
+        values(s, take(), KIND != kExact && j >= 2, true);
         if (j + 2 < sh.n) scores(s, take(), true);
       }
     }
-    if (elect_one()) {
+    if (KIND != kExact && elect_one()) {
       tc_commit(&sm.o_full);
       mbar_arrive(&sm.o_full);
     }
@@ -445,16 +493,204 @@ __device__ __forceinline__ uint64_t nodes_seen(const AttnParams& p, int b, int c
   return t < 0 ? 0 : t < 32 ? a : c;
 }
 
-template <int D, bool TWO>
+// The queries of row r of a row block into shared memory (columns 8 first to 8 end),
+// swizzled, in PARTS bf16 parts; a row that is not there is zero.
+template <int D, int PARTS>
+__device__ __forceinline__ void load_query(const AttnParams& p, const Share& sh, int row, bool live,
+                                           int r, uint8_t* block, int first = 0, int end = D / 8) {
+  uint8_t* dst = block + r * 128;
+  const int64_t off = live ? row_offset(p, sh.b, sh.g, row, D, p.qs) : 0;
+#pragma unroll 4
+  for (int c = first; c < end; ++c) {
+    uint4 w[PARTS];
+    if constexpr (PARTS == 1) {
+      w[0] = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)p.q + off) + c);
+    } else {
+      const float4* src = reinterpret_cast<const float4*>((const float*)p.q + off) + 2 * c;
+      const float4 a = __ldg(src), b = __ldg(src + 1);
+      uint32_t x[4][PARTS];
+      split(a.x, a.y, x[0]);
+      split(a.z, a.w, x[1]);
+      split(b.x, b.y, x[2]);
+      split(b.z, b.w, x[3]);
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) w[q] = make_uint4(x[0][q], x[1][q], x[2][q], x[3][q]);
+    }
+#pragma unroll
+    for (int q = 0; q < PARTS; ++q)
+      *reinterpret_cast<uint4*>(dst + q * 128 * D * 2 + (c / 8) * (128 * 128) +
+                                (((c % 8) ^ (r & 7)) * 16)) = live ? w[q] : make_uint4(0, 0, 0, 0);
+  }
+  fence_async_smem();
+}
+
+// What a row sees of a tile: the context keys below `off` (the first node's place
+// in the tile), the nodes of `seen`, of the keys that are there.
+struct Sight {
+  bool some;  // not simply all
+  uint32_t bits[4];
+};
+__device__ __forceinline__ Sight sight_of(const uint32_t (&mask)[4], int off, uint64_t seen) {
+  const uint4 there = *reinterpret_cast<const uint4*>(mask);
+  Sight v;
+  v.some = (there.x & there.y & there.z & there.w) != 0xffffffffu || off < kKeys;
+  v.bits[0] = v.bits[1] = v.bits[2] = v.bits[3] = ~0u;
+  if (v.some) {
+    uint64_t lo, hi;
+    if (off >= 128) lo = hi = ~0ull;
+    else if (off >= 64) {
+      lo = ~0ull;
+      hi = off == 64 ? seen : ((1ull << (off - 64)) - 1) | seen << (off - 64);
+    } else if (off > 0) {
+      lo = ((1ull << off) - 1) | seen << off;
+      hi = seen >> (64 - off);
+    } else {
+      lo = off > -64 ? seen >> -off : 0;
+      hi = 0;
+    }
+    v.bits[0] = (uint32_t)lo & there.x, v.bits[1] = (uint32_t)(lo >> 32) & there.y;
+    v.bits[2] = (uint32_t)hi & there.z, v.bits[3] = (uint32_t)(hi >> 32) & there.w;
+  }
+  return v;
+}
+
+// Reads N scores of the lane's row, those it does not see (bits) as -inf, and
+// returns their maximum.
+template <int N>
+__device__ __forceinline__ float read_scores(uint32_t at, bool some, const uint32_t* bits,
+                                             uint32_t (&x)[N]) {
+#pragma unroll
+  for (int h = 0; h < N / 32; ++h) tmem_load32(at + 32 * h, x + 32 * h);
+  tmem_wait_ld();
+  if (some) {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (!(bits[e / 32] >> (e % 32) & 1)) x[e] = 0xff800000u;  // -inf
+  }
+  float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < N; e += 8)
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      tops[h] = max3(tops[h], __uint_as_float(x[e + 2 * h]), __uint_as_float(x[e + 2 * h + 1]));
+  return fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+}
+
+// Moves the reference m where the tile's maximum asks for it and returns the
+// factor of what was summed under the old one.
+__device__ __forceinline__ float move_reference(float top, float& m, float& l) {
+  if (!(top > m + kSlack) && m != -INFINITY) return 1.f;
+  const float keep = m == -INFINITY ? 0.f : fast_exp2(m - top);  // 0 at the first key
+  m = top;
+  l *= keep;
+  return keep;
+}
+
+// The weights of two neighbouring keys, added to the sum
+__device__ __forceinline__ float2 weights2(uint32_t a, uint32_t b, unsigned long long scale2,
+                                           unsigned long long from2, unsigned long long& sum) {
+  unsigned long long z = from2;
+  ffma2(z, pack2(__uint_as_float(a), __uint_as_float(b)), scale2);
+  float2 w = unpack2(z);
+  w.x = fast_exp2(w.x);
+  w.y = fast_exp2(w.y);
+  add2(sum, pack2(w.x, w.y));
+  return w;
+}
+
+// Two weights (finite, not negative) as three bf16 parts each: the upper 8 bits of
+// the significand, the next 8, the last 8, so the parts' sum is the weight.
+__device__ __forceinline__ void split_exactly(float2 w, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const uint32_t x = __float_as_uint(w.x), y = __float_as_uint(w.y);
+  a = __byte_perm(x, y, 0x7632);  // the upper halves
+  unsigned long long rest = pack2(w.x, w.y);
+  add2(rest, pack2(-__uint_as_float(x & 0xffff0000u), -__uint_as_float(y & 0xffff0000u)));
+  const float2 r = unpack2(rest);
+  const uint32_t rx = __float_as_uint(r.x), ry = __float_as_uint(r.y);
+  b = __byte_perm(rx, ry, 0x7632);
+  add2(rest, pack2(-__uint_as_float(rx & 0xffff0000u), -__uint_as_float(ry & 0xffff0000u)));
+  const float2 q = unpack2(rest);
+  c = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632);
+}
+
+// 32 columns of a finished row: the odd values it sees added, then written out
+// (whole: divided by the sum, in the type of the call) or to the workspace.
+template <int D, int PARTS>
+__device__ __forceinline__ void put_columns(const AttnParams& p, const Share& sh, const Shared& sm,
+                                            uint32_t share, uint64_t seen, int row, int c, bool live,
+                                            float l, size_t slot, float (&y)[32]) {
+  if (sm.odd[share & 1]) {
+    for (uint64_t left = seen; left; left &= left - 1) {
+      const int node = __ffsll((long long)left) - 1;
+      const uint32_t up = sm.odd_at[share & 1][node][0][c / 32];
+      const uint32_t down = sm.odd_at[share & 1][node][1][c / 32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        if (up >> e & 1) y[e] += INFINITY;
+        if (down >> e & 1) y[e] -= INFINITY;
+      }
+    }
+  }
+  if (live && sh.n == sh.nt) {
+    const int64_t off = row_offset(p, sh.b, sh.g, row, D, p.os) + c;
+    const float scale = 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) y[e] = l == 0.f ? 0.f : y[e] * scale;  // 0: no key seen
+    if constexpr (PARTS > 1) {
+      float4* dst = reinterpret_cast<float4*>((float*)p.out + off);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>((uint16_t*)p.out + off);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        dst[e] = make_uint4(bf16x2_rn(y[8 * e], y[8 * e + 1]), bf16x2_rn(y[8 * e + 2], y[8 * e + 3]),
+                            bf16x2_rn(y[8 * e + 4], y[8 * e + 5]), bf16x2_rn(y[8 * e + 6], y[8 * e + 7]));
+    }
+  } else if (live) {
+    float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+  }
+  __syncwarp();
+}
+
+// The end of a share, for the eight warps of the rows: the list of odd values is
+// cleared for the share after next, and what the share used is free again.
+__device__ __forceinline__ void end_share(Shared& sm, uint32_t share) {
+  named_bar(1, 32 * kSoftWarps);
+  if (sm.odd[share & 1]) {
+    for (int i = threadIdx.x; i < MK_MAX_TREE * 8; i += 32 * kSoftWarps)
+      (&sm.odd_at[share & 1][0][0][0])[i] = 0;
+    named_bar(1, 32 * kSoftWarps);
+    if (threadIdx.x == 0) sm.odd[share & 1] = 0;
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(&sm.done[share & 1]);
+}
+
+__device__ __forceinline__ bool wait_failed(Shared& sm) {
+  return *reinterpret_cast<volatile int*>(&sm.failed) != 0;
+}
+
+// kOne, kTwo: softmax of a stream.
+template <int D, int KIND>
 __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, const int* prefix,
                                              uint8_t* q_ptr, uint32_t tmem, int u_begin,
                                              int u_end, int rt, int group) {
+  using Lay = Layout<D, KIND>;
+  constexpr bool TWO = Lay::TWO;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int stream = warp / 4, r = (warp % 4) * 32 + lane;  // row of the stream's block
   const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
-  const uint32_t t_s = tmem + lanes + stream * kKeys, t_o = tmem + lanes + 2 * kKeys + stream * D;
+  const uint32_t t_s = tmem + lanes + stream * Lay::kScoreStep;
+  const uint32_t t_o = tmem + lanes + Lay::kOut + stream * D;
   const int block_rows = TWO ? p.row_tile / 2 : 128;       // rows of a stream's block
   const int local = TWO ? stream * block_rows + r : r;     // row of the row tile
+  const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2);
   Waiter wait(sm);
   uint32_t s_uses = 0, tile_no = 0;
   int u = u_begin;
@@ -464,18 +700,8 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
     const int row = rt * p.row_tile + local;
     const bool live = r < block_rows && row < sh.rows;
     const bool warp_live = __any_sync(0xffffffffu, live);
-
-    // ---- the row's queries, swizzled; rows that are not there are zero
-    if (TWO || stream == 0) {
-      uint8_t* dst = q_ptr + (TWO ? stream * 128 * D * 2 : 0) + r * 128;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          (const uint16_t*)p.q + (live ? row_offset(p, sh.b, sh.g, row, D, p.qs) : 0));
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c)
-        *reinterpret_cast<uint4*>(dst + (c / 8) * (128 * 128) + (((c % 8) ^ (r & 7)) * 16)) =
-            live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-      fence_async_smem();
-    }
+    if (TWO || stream == 0)
+      load_query<D, 1>(p, sh, row, live, r, q_ptr + (TWO ? stream * 128 * D * 2 : 0));
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full);
     const uint64_t seen = nodes_seen(p, sh.b, sh.count, live ? row / p.G : -1);
@@ -486,48 +712,9 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
       tc_fence_after();
       if (warp_live) {
         uint32_t x[kKeys];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) tmem_load32(t_s + 32 * h, x + 32 * h);
-        const uint4 there = *reinterpret_cast<const uint4*>(sm.mask[(tile_no + j) % kMasks]);
-        const int off = sh.start - (sh.k0 + j) * kKeys;  // first node's place in the tile
-        const bool some = (there.x & there.y & there.z & there.w) != 0xffffffffu || off < kKeys;
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        if (some) {
-          // context keys below `off`, then the nodes that the row sees
-          uint64_t lo, hi;
-          if (off >= 128) lo = hi = ~0ull;
-          else if (off >= 64) {
-            lo = ~0ull;
-            hi = off == 64 ? seen : ((1ull << (off - 64)) - 1) | seen << (off - 64);
-          } else if (off > 0) {
-            lo = ((1ull << off) - 1) | seen << off;
-            hi = seen >> (64 - off);
-          } else {
-            lo = off > -64 ? seen >> -off : 0;
-            hi = 0;
-          }
-          see[0] = (uint32_t)lo & there.x, see[1] = (uint32_t)(lo >> 32) & there.y;
-          see[2] = (uint32_t)hi & there.z, see[3] = (uint32_t)(hi >> 32) & there.w;
-        }
-        tmem_wait_ld();
-        if (some) {
-#pragma unroll
-          for (int e = 0; e < kKeys; ++e)
-            if (!(see[e / 32] >> (e % 32) & 1)) x[e] = 0xff800000u;  // -inf
-        }
-        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int e = 0; e < kKeys; e += 8)
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            tops[h] = max3(tops[h], __uint_as_float(x[e + 2 * h]), __uint_as_float(x[e + 2 * h + 1]));
-        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * p.scale_log2;
-        float keep = 1.f;
-        if (top > m + kSlack || m == -INFINITY) {
-          keep = m == -INFINITY ? 0.f : fast_exp2(m - top);  // 0 at the first key
-          m = top;
-          l *= keep;
-        }
+        const Sight v = sight_of(sm.mask[(tile_no + j) % kMasks], sh.start - (sh.k0 + j) * kKeys, seen);
+        const float top = read_scores(t_s, v.some, v.bits, x);
+        const float keep = move_reference(top * p.scale_log2, m, l);
         const int before = TWO ? j : j / 2;  // tiles already in O
         if (before > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll 1
@@ -541,7 +728,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
           }
         }
         const float from = m == -INFINITY ? 0.f : -m;
-        const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2), from2 = pack2(from, from);
+        const unsigned long long from2 = pack2(from, from);
         unsigned long long sums[2] = {0, 0};
         __syncwarp();
 #pragma unroll
@@ -549,16 +736,11 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
           uint32_t w[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            unsigned long long z = from2;
-            ffma2(z, pack2(__uint_as_float(x[64 * h + 2 * e]), __uint_as_float(x[64 * h + 2 * e + 1])), scale2);
-            float2 a = unpack2(z);
-            a.x = fast_exp2(a.x);
-            a.y = fast_exp2(a.y);
-            add2(sums[e % 2], pack2(a.x, a.y));
+            const float2 a = weights2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
             w[e] = bf16x2_rn(a.x, a.y);
           }
           tmem_store32(t_s + 32 * h, w);
-          if (h == 0) {  // the products of the first half need not wait for the second
+          if (h == 0) {  // its products need not wait for the second half
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -586,94 +768,165 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
     wait(&sm.o_full, share);
     tc_fence_after();
     if (!TWO) named_bar(1, 32 * kSoftWarps);
-    const bool writes = TWO || stream == 0;
-    if (writes && warp_live) {
+    if ((TWO || stream == 0) && warp_live) {
       float f0 = 1.f, f1 = 0.f;  // factors of the streams' shares (one row block)
-      float l1 = 0.f;
       if (!TWO) {
-        const float m1 = sm.ml[r][0];
-        l1 = sm.ml[r][1];
+        const float m1 = sm.ml[r][0], l1 = sm.ml[r][1];
         const float both = fmaxf(m, m1);
         f0 = l == 0.f ? 0.f : fast_exp2(m - both);
         f1 = l1 == 0.f ? 0.f : fast_exp2(m1 - both);
         l = (l == 0.f ? 0.f : l * f0) + (l1 == 0.f ? 0.f : l1 * f1);
         m = both;
+      } else if (l == 0.f) {
+        f0 = 0.f;
       }
-      if (*reinterpret_cast<volatile int*>(&sm.failed)) l = NAN;
-      const bool any0 = TWO ? l != 0.f : true, any1 = !TWO && sh.n > 1;
-      const bool whole = sh.n == sh.nt;
-      const float scale = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-      const uint32_t odd = sm.odd[share & 1];
+      if (wait_failed(sm)) l = NAN;
+      const bool second = !TWO && sh.n > 1;  // stream 1 had a tile
       const size_t slot = part_slot(p, group, sh.begins, rt) * p.row_tile + local;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32], o1[32];
         tmem_load32(t_o + c, o);
-        if (!TWO && any1) tmem_load32(t_o + D + c, o1);
+        if (second) tmem_load32(t_o + D + c, o1);
         tmem_wait_ld();
         float y[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          y[e] = any0 && f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
-          if (!TWO && any1 && f1 != 0.f) y[e] += __uint_as_float(o1[e]) * f1;
+          y[e] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
+          if (second && f1 != 0.f) y[e] += __uint_as_float(o1[e]) * f1;
         }
-        if (odd) {
-          for (uint64_t left = seen; left; left &= left - 1) {
-            const int node = __ffsll((long long)left) - 1;
-            const uint32_t up = sm.odd_at[share & 1][node][0][c / 32];
-            const uint32_t down = sm.odd_at[share & 1][node][1][c / 32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (up >> e & 1) y[e] += INFINITY;
-              if (down >> e & 1) y[e] -= INFINITY;
-            }
-          }
-        }
-        if (live && whole) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            w[e] = bf16x2_rn(y[2 * e] * scale, y[2 * e + 1] * scale);
-            if (l == 0.f) w[e] = 0;  // no key seen
-          }
-          uint4* dst = reinterpret_cast<uint4*>((uint16_t*)p.out +
-                                                row_offset(p, sh.b, sh.g, row, D, p.os) + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        } else if (live) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-        }
-        __syncwarp();
+        put_columns<D, 1>(p, sh, sm, share, seen, row, c, live, l, slot, y);
       }
-      if (live && !whole) {
+      if (live && sh.n != sh.nt) {
         p.part_ml[slot * 2] = m;
         p.part_ml[slot * 2 + 1] = l;
       }
     }
-    // The list of odd values is cleared for the share after next, O may be
-    // overwritten. (All of a stream's readers of the list are behind this
-    // barrier.)
-    named_bar(1, 32 * kSoftWarps);
-    if (sm.odd[share & 1]) {
-      for (int i = threadIdx.x; i < MK_MAX_TREE * 8; i += 32 * kSoftWarps)
-        (&sm.odd_at[share & 1][0][0][0])[i] = 0;
-      named_bar(1, 32 * kSoftWarps);
-      if (threadIdx.x == 0) sm.odd[share & 1] = 0;
-    }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.done[share & 1]);
+    end_share(sm, share);
     ++share;
   }
 }
 
-template <int D, bool TWO>
+// kExact: a row has two threads, half 0 in warps 0-3 and half 1 in warps 4-7. Each
+// makes the weights of half of every tile's keys (their maxima meet in shared
+// memory) and keeps half of the row's output columns in registers, to which it
+// adds a tile's product while the next one is made.
+template <int D>
+__device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, const int* prefix,
+                                           uint8_t* q_ptr, uint32_t tmem, int u_begin, int u_end,
+                                           int rt, int group) {
+  using Lay = Layout<D, kExact>;
+  const int half = threadIdx.x / 128, r = threadIdx.x % 128, lane = threadIdx.x % 32;
+  const uint32_t lanes = (uint32_t)(r / 32) * 32 << 16;
+  const uint32_t t_o = tmem + lanes + Lay::kOut + half * (D / 2);
+  const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2);
+  Waiter wait(sm);
+  uint32_t s_uses[2] = {0, 0}, tile_no = 0;
+  int u = u_begin;
+  Share sh;
+  for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
+    if (rt * p.row_tile >= sh.rows) continue;
+    const int row = rt * p.row_tile + r;
+    const bool live = row < sh.rows, warp_live = __any_sync(0xffffffffu, live);
+    load_query<D, 3>(p, sh, row, live, r, q_ptr, half * (D / 16), (half + 1) * (D / 16));
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_full);
+    const uint64_t seen = nodes_seen(p, sh.b, sh.count, live ? row / p.G : -1);
+    float m = -INFINITY, l = 0.f, keep = 1.f, acc[D / 2];
+#pragma unroll
+    for (int e = 0; e < D / 2; ++e) acc[e] = 0.f;
+    for (int j = 0; j <= sh.n; ++j) {
+      const float last_keep = keep;  // the factor of the tile before
+      if (j < sh.n) {
+        const int s = j & 1;
+        const uint32_t t_s = tmem + lanes + s * Lay::kScoreStep;
+        wait(&sm.s_full[s], s ? s_uses[1]++ : s_uses[0]++);
+        tc_fence_after();
+        uint32_t x[64];
+        float top = -INFINITY;
+        if (warp_live) {
+          const Sight v = sight_of(sm.mask[(tile_no + j) % kMasks], sh.start - (sh.k0 + j) * kKeys, seen);
+          const uint32_t bits[2] = {half ? v.bits[2] : v.bits[0], half ? v.bits[3] : v.bits[1]};
+          top = read_scores(t_s + 64 * half, v.some, bits, x);
+          sm.top[s][half][r] = top;
+        }
+        // both halves' scores have been read (the weights go over them), both
+        // maxima are there
+        tc_fence_before();
+        named_bar(1, 32 * kSoftWarps);
+        tc_fence_after();
+        if (warp_live) {
+          keep = move_reference(fmaxf(top, sm.top[s][half ^ 1][r]) * p.scale_log2, m, l);
+          const float from = m == -INFINITY ? 0.f : -m;
+          const unsigned long long from2 = pack2(from, from);
+          unsigned long long sums[2] = {0, 0};
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[3][16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float2 a = weights2(x[32 * h + 2 * e], x[32 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
+              split_exactly(a, w[0][e], w[1][e], w[2][e]);
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q) tmem_store16(t_s + q * 64 + 32 * half + 16 * h, w[q]);
+          }
+          add2(sums[0], sums[1]);
+          const float2 sum = unpack2(sums[0]);
+          l += sum.x + sum.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[s][half]);
+      }
+      if (j > 0) {
+        wait(&sm.t_full, tile_no + j - 1);
+        tc_fence_after();
+        if (warp_live) {
+#pragma unroll
+          for (int c = 0; c < D / 2; c += 32) {
+            uint32_t t[32];
+            tmem_load32(t_o + c, t);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[c + e] = fmaf(acc[c + e], last_keep, __uint_as_float(t[e]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.t_free);
+      }
+    }
+    tile_no += sh.n;
+    sm.sum[half][r] = l;
+    named_bar(1, 32 * kSoftWarps);
+    if (warp_live) {
+      l = sm.sum[0][r] + sm.sum[1][r];
+      if (wait_failed(sm)) l = NAN;
+      const size_t slot = part_slot(p, group, sh.begins, rt) * p.row_tile + r;
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 32) {
+        float y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = l == 0.f ? 0.f : acc[c + e];
+        put_columns<D, 3>(p, sh, sm, share, seen, row, half * (D / 2) + c, live, l, slot, y);
+      }
+      if (live && sh.n != sh.nt && half == 0) {
+        p.part_ml[slot * 2] = m;
+        p.part_ml[slot * 2 + 1] = l;
+      }
+    }
+    end_share(sm, share);
+    ++share;
+  }
+}
+
+template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
-  using Lay = Layout<D, TWO>;
+  using Lay = Layout<D, KIND>;
   extern __shared__ uint8_t raw[];
   __shared__ Shared sm;
   __shared__ int prefix[kMaxSeqs + 1];
@@ -698,6 +951,8 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
     }
     mbar_init(&sm.q_full, kSoftWarps);
     mbar_init(&sm.o_full, 2);
+    mbar_init(&sm.t_full, 2);
+    mbar_init(&sm.t_free, kSoftWarps);
     sm.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -716,14 +971,18 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   // copy, because each waited for the last one's operands to be read).
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    softmax_role<D, TWO>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
+    if constexpr (KIND == kExact) {
+      exact_role<D>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
+    } else {
+      softmax_role<D, KIND>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
+    }
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    load_role<D, TWO>(p, sm, prefix, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
+    load_role<D, KIND>(p, sm, prefix, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kMmaWarp)
-      mma_role<D, TWO>(p, sm, prefix, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
+      mma_role<D, KIND>(p, sm, prefix, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
   }
   tc_fence_before();
   __syncthreads();
@@ -731,10 +990,10 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-template <int D, bool TWO>
+template <int D, int KIND>
 int launch(const AttnParams& p, cudaStream_t st) {
-  using Lay = Layout<D, TWO>;
-  auto* fn = tree_attention_tc_kernel<D, TWO>;
+  using Lay = Layout<D, KIND>;
+  auto* fn = tree_attention_tc_kernel<D, KIND>;
   static std::atomic<uint64_t> ready{0};
   if (int rc = allow_shared(ready, (const void*)fn, Lay::kBytes)) return rc;
   fn<<<p.groups * p.row_tiles, kThreads, Lay::kBytes, st>>>(p);
@@ -743,10 +1002,15 @@ int launch(const AttnParams& p, cudaStream_t st) {
 
 }  // namespace
 
-int launch_tree_attention_tc(const AttnParams& p, int head_dim, cudaStream_t st) {
+int launch_tree_attention_tc(const AttnParams& p, int head_dim, int type, cudaStream_t st) {
   const bool two = p.row_tile > 128;
-  if (head_dim == 64) return two ? launch<64, true>(p, st) : launch<64, false>(p, st);
-  return two ? launch<128, true>(p, st) : launch<128, false>(p, st);
+  if (head_dim == 64)
+    return type == MK_TYPE_FP32 ? launch<64, kExact>(p, st)
+           : two                ? launch<64, kTwo>(p, st)
+                                : launch<64, kOne>(p, st);
+  return type == MK_TYPE_FP32 ? launch<128, kExact>(p, st)
+         : two                ? launch<128, kTwo>(p, st)
+                              : launch<128, kOne>(p, st);
 }
 
 }  // namespace mk

@@ -674,14 +674,18 @@ def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
     need = ctypes.c_size_t()
     _check(lib().mk_tree_accept_workspace(b, n, vocab, ctypes.byref(need)))
+    # one allocation: the workspace (a few KB), then the outputs behind it
+    first, rows = -(-need.value // 4), b * n
     with _Call(dev, stream) as call:
-        ws = call.new(need.value, torch.uint8)
-        nodes, seqs = call.new((2, b, n), torch.int32), call.new((2, b), torch.int32)
-        at, to = nodes.data_ptr(), seqs.data_ptr()
+        buf = call.new(first + 2 * rows + 2 * b, torch.int32)
+        ws = buf.data_ptr()
+        at = ws + 4 * first
         _check(lib().mk_tree_accept(b, n, vocab, kind, logits.data_ptr(), stride, tp, pp, cp, at,
-                                    at + 4 * b * n, to, to + 4 * b, ws.data_ptr(), need.value,
-                                    call.raw))
-    return (*nodes.unbind(), *seqs.unbind())
+                                    at + 4 * rows, at + 8 * rows, at + 8 * rows + 4 * b, ws,
+                                    need.value, call.raw))
+    last = first + 2 * rows
+    return (buf.as_strided((b, n), (n, 1), first), buf.as_strided((b, n), (n, 1), first + rows),
+            buf.as_strided((b,), (1,), last), buf.as_strided((b,), (1,), last + b))
 
 
 def cache_compact(cache: Cache, starts, path, accepted, stream=None):
@@ -698,14 +702,28 @@ def cache_compact(cache: Cache, starts, path, accepted, stream=None):
         _check(lib().mk_cache_compact(cache.ref, b, n, sp, pp, ap, call.raw))
 
 
+def _host_ints(x) -> np.ndarray:
+    """A contiguous host int32 array of x (whole numbers only)."""
+    a = np.asarray(x)
+    if a.dtype != np.int32:
+        if a.size and (a.dtype.kind not in "iu" or a.min() < -2**31 or a.max() >= 2**31):
+            raise _bad("host arrays must hold 32-bit whole numbers")
+        a = a.astype(np.int32)
+    return np.ascontiguousarray(a)
+
+
+def _at(a: np.ndarray) -> int:
+    return a.__array_interface__["data"][0]
+
+
 def cache_copy_blocks(cache: Cache, copies, stream=None):
     """mk_cache_copy_blocks: copies [n][3] on the host, (src, dst, rows) each, as
     the calls of Pages return them."""
-    c = np.ascontiguousarray(copies, dtype=np.int32)
+    c = _host_ints(copies)
     if c.size and (c.ndim != 2 or c.shape[1] != 3):
         raise _bad("copies must be [n][3]")
     with _Call(cache.device, stream) as call:
-        _check(lib().mk_cache_copy_blocks(cache.ref, c.ctypes.data, c.size // 3, call.raw))
+        _check(lib().mk_cache_copy_blocks(cache.ref, _at(c), c.size // 3, call.raw))
 
 
 class Pages:
@@ -723,8 +741,8 @@ class Pages:
 
     @staticmethod
     def _pair(a, b, what: str):
-        a, b = (np.ascontiguousarray(np.atleast_1d(x), dtype=np.int32) for x in (a, b))
-        if a.ndim != 1 or a.shape != b.shape:
+        a, b = _host_ints(a).reshape(-1), _host_ints(b).reshape(-1)
+        if a.shape != b.shape:
             raise _bad(f"{what} must be two lists of the same length")
         return a, b
 
@@ -732,31 +750,30 @@ class Pages:
         """mk_pages_resize (0: gives a sequence's pages back)."""
         s, n = self._pair(seqs, lengths, "seqs, lengths")
         copies, made = np.empty((len(s), 3), np.int32), ctypes.c_int()
-        _check(lib().mk_pages_resize(self.h, len(s), s.ctypes.data, n.ctypes.data,
-                                     copies.ctypes.data, len(s), ctypes.byref(made)))
+        _check(lib().mk_pages_resize(self.h, len(s), _at(s), _at(n), _at(copies), len(s),
+                                     ctypes.byref(made)))
         return copies[:made.value]
 
     def fork(self, parents, children):
         """mk_pages_fork: each empty child becomes a fork of its parent."""
         p, c = self._pair(parents, children, "parents, children")
-        _check(lib().mk_pages_fork(self.h, len(p), p.ctypes.data, c.ctypes.data))
+        _check(lib().mk_pages_fork(self.h, len(p), _at(p), _at(c)))
 
     def compact(self) -> np.ndarray:
         """mk_pages_compact: the pages in use renumbered to the lowest ones."""
         copies, made = np.empty((self.n_blocks, 3), np.int32), ctypes.c_int()
-        _check(lib().mk_pages_compact(self.h, copies.ctypes.data, self.n_blocks,
-                                      ctypes.byref(made)))
+        _check(lib().mk_pages_compact(self.h, _at(copies), self.n_blocks, ctypes.byref(made)))
         return copies[:made.value]
 
     def table(self) -> np.ndarray:
         """[n_seqs][entries] int32, -1 behind a sequence's pages."""
         t = np.empty((self.n_seqs, self.entries), np.int32)
-        _check(lib().mk_pages_read(self.h, t.ctypes.data, None, None))
+        _check(lib().mk_pages_read(self.h, _at(t), None, None))
         return t
 
     def lengths(self) -> np.ndarray:
         n = np.empty(self.n_seqs, np.int32)
-        _check(lib().mk_pages_read(self.h, None, n.ctypes.data, None))
+        _check(lib().mk_pages_read(self.h, None, _at(n), None))
         return n
 
     def n_free(self) -> int:
