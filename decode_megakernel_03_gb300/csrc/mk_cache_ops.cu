@@ -100,10 +100,10 @@ enum { kNeighbours, kHalves, kHalvesOdd };
 // that it is exact to 2^-64 turns at any position), then every head of q, k and
 // v, eight elements per lane, one head in D / 8 neighbouring lanes. All of a
 // head's loads come before its first store, so q_out may be q.
-// Bound by the bytes of the rows; two heads are in flight per lane.
+// Bound by the bytes of the rows; four heads are in flight per lane (two: 4 % slower).
 template <typename T, int D, int PAIRS>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 2;
+  constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
   __shared__ float2 cs[kRopeTokens][D / 2];
   __shared__ int s_pos[kRopeTokens];
   __shared__ uint32_t s_row[kRopeTokens];

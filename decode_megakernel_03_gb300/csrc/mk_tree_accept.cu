@@ -116,16 +116,26 @@ struct WalkParams {
   int T, splits;
 };
 
-// One block per sequence: the splits' keys joined, one warp per node at a time,
-// then one warp walks. A chain (no parents) may have any length: its nodes are
+// One block per sequence: the splits' keys joined, one of 32 warps per node at a
+// time, then one warp walks. A chain (no parents) may have any length: its nodes are
 // taken 32 at a time. In a tree, lane l holds nodes l and l + 32; the children
 // whose token fits are found by a ballot, the lowest one first.
-__global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ WalkParams p) {
-  griddep_wait();
+constexpr int kWalkThreads = 1024;
+
+__global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constant__ WalkParams p) {
+  __shared__ int s_choice[MK_MAX_TREE];
   const int b = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n = clamped(p.counts, b, p.T);
   const int64_t base = (int64_t)b * p.T;
-  for (int t = warp; t < p.T; t += kThreads / 32) {
+  // of a tree, lane l of the walking warp holds nodes l and l + 32
+  const bool tree = p.parents != nullptr, has0 = lane < n, has1 = lane + 32 < n;
+  int par0 = -1, par1 = -1, tok0 = 0, tok1 = 0;
+  if (warp == 0 && tree) {
+    if (has0) par0 = __ldg(p.parents + base + lane), tok0 = __ldg(p.tokens + base + lane);
+    if (has1) par1 = __ldg(p.parents + base + lane + 32), tok1 = __ldg(p.tokens + base + lane + 32);
+  }
+  griddep_wait();
+  for (int t = warp; t < p.T; t += kWalkThreads / 32) {
     uint64_t key = 0;
     if (t < n)
       for (int s = lane; s < p.splits; s += 32)
@@ -133,7 +143,9 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
 #pragma unroll
     for (int d = 16; d; d /= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, d));
     if (lane == 0) {
-      p.choices[base + t] = t < n ? (int)(0xffffffffu - (uint32_t)key) : -1;
+      const int c = t < n ? (int)(0xffffffffu - (uint32_t)key) : -1;
+      p.choices[base + t] = c;
+      if (tree) s_choice[t] = c;  // a tree has at most MK_MAX_TREE nodes
       p.path[base + t] = -1;
     }
   }
@@ -144,15 +156,10 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
   if (n > 0) {
     cur = 0;
     taken = 1;
-    if (p.parents) {
-      const int32_t* par = p.parents + base;
-      const bool has0 = lane < n, has1 = lane + 32 < n;
-      const int par0 = has0 ? par[lane] : -1, par1 = has1 ? par[lane + 32] : -1;
-      const int tok0 = has0 ? tok[lane] : 0, tok1 = has1 ? tok[lane + 32] : 0;
-      const int ch0 = has0 ? choice[lane] : 0, ch1 = has1 ? choice[lane + 32] : 0;
+    if (tree) {
       if (lane == 0) p.path[base] = 0;
       for (;;) {
-        const int want = __shfl_sync(0xffffffffu, cur < 32 ? ch0 : ch1, cur & 31);
+        const int want = s_choice[cur];
         const unsigned f0 = __ballot_sync(0xffffffffu, has0 && lane > cur && par0 == cur && tok0 == want);
         const unsigned f1 = __ballot_sync(0xffffffffu, has1 && lane + 32 > cur && par1 == cur && tok1 == want);
         if (!(f0 | f1)) break;
@@ -180,11 +187,11 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(const __grid_constant__ 
   }
 }
 
-// Splits of a row: as many as make about eight blocks per SM of a 152-SM
-// machine, none shorter than 4096 values (16 KB of fp32: shorter ones spend
-// their time starting up).
+// Splits of a row: as many as make about 32 blocks per SM of a 152-SM machine (four
+// times what is resident at once, so that the SMs finish together), none shorter
+// than 4096 values (16 KB of fp32: shorter ones spend their time starting up).
 int splits_of(int rows, int V) {
-  const int want = std::max(1, 8 * 152 / std::max(1, rows));
+  const int want = std::max(1, 32 * 152 / std::max(1, rows));
   return std::min(want, std::max(1, V / 4096));
 }
 
@@ -258,7 +265,7 @@ int mk_tree_accept(int batch, int n_tokens, int vocab, int type, const void* log
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(batch);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kWalkThreads);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -10,9 +10,9 @@
 namespace mk {
 namespace {
 
-constexpr int kTile = 64;        // keys of a tile
 constexpr int kStages = 3;       // tiles in shared memory
-constexpr int kThreads = 128;    // four warps, each 16 keys of a tile
+constexpr int kThreads = 128;    // four warps, each a quarter of a tile's keys
+constexpr int kRows = 16;        // rows of a row tile
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxG = 8;
 
@@ -28,27 +28,32 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 }
 
 // ---- the kernel ------------------------------------------------------------------------
-// MT m16 row blocks per row tile; P = 1: bf16 activations; P = 3: fp32 ones,
-// queries and weights as three bf16 parts (2^-24 of the value: fp32's own
-// step; the cache is bf16, so products of parts are exact).
-// Weights of bf16 calls are rounded to bf16 (relative 2^-8, the size of the
-// output's own rounding); sums, maxima and the output accumulate in fp32.
-template <int D, int MT, int P>
+// One m16 block of rows. P = 1: bf16 activations; P = 3: fp32 ones, queries and
+// weights as three bf16 parts (2^-24 of the value: fp32's own step; the cache is
+// bf16, so products of parts are exact). Weights of bf16 calls are rounded to
+// bf16 (relative 2^-8, the size of the output's own rounding); sums, maxima and
+// the output accumulate in fp32. A tile is 16 KB of keys and 16 KB of values
+// whatever the head's size: 64-key tiles of 64 dimensions spent their time on the
+// barriers between them.
+constexpr int tile_keys(int D) { return 8192 / D; }
+
+template <int D, int P>
 struct Layout {
-  static constexpr int RT = 16 * MT;
+  static constexpr int kTile = tile_keys(D);
   static constexpr int kStageBytes = 2 * kTile * D * 2;
   static constexpr int kRing = kStages * kStageBytes;
-  // joined warps: o [4][RT][D] fp32 over the ring
-  static_assert(4 * RT * D * 4 <= kRing, "the warps' shares fit the ring");
+  // joined warps: o [4][kRows][D] fp32 over the ring
+  static_assert(4 * kRows * D * 4 <= kRing, "the warps' shares fit the ring");
   static constexpr int kRowTab = (kStages + 1) * kTile * 4;
   static constexpr int kBytes = kRing + kRowTab;
 };
 
-template <int D, int MT, int P>
+template <int D, int P>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 tree_attention_kernel(const __grid_constant__ AttnParams p) {
-  using Lay = Layout<D, MT, P>;
-  constexpr int RT = Lay::RT, KB = D / 16, NB = D / 8;
+  using Lay = Layout<D, P>;
+  constexpr int kTile = Lay::kTile, RT = kRows, KB = D / 16, NB = D / 8;
+  constexpr int NK = kTile / 64;  // blocks of 16 keys that a warp takes of a tile
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t* rowtab = reinterpret_cast<uint32_t*>(smem + Lay::kRing);  // [kStages + 1][kTile]
   __shared__ int prefix[kMaxSeqs + 1];
@@ -123,36 +128,13 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
     __syncthreads();
 #pragma unroll
     for (int it = 0; it < kStages - 1; ++it) fetch(it);
-    for (int i = 0; i < 6; ++i) {
-      uint64_t seen = 0;
-      int up = -1;
-      if (tid < MK_MAX_TREE) {
-        up = s_up[tid];
-        seen = s_seen[tid];
-        if (up >= 0) {
-          seen |= s_seen[up];
-          up = s_up[up];
-        }
-      }
-      __syncthreads();
-      if (tid < MK_MAX_TREE) {
-        s_up[tid] = up;
-        s_seen[tid] = seen;
-      }
-      __syncthreads();
-    }
-
-    // ---- the rows' queries as A fragments, and what they see
-    uint4 qf[P][MT][KB];
-    uint64_t seen[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    // ---- the rows' queries as A fragments, and what the rows see
+    uint4 qf[P][KB];
+    {
       const void* src[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = rt * RT + m * 16 + h * 8 + grp;
-        const int t = r / p.G;
-        seen[m][h] = r < rows ? s_seen[t] : 0;
+        const int r = rt * RT + h * 8 + grp;
         const int64_t off = row_offset(p, b, g, r, D, p.qs);
         src[h] = r >= rows ? nullptr
                  : P > 1    ? (const void*)((const float*)p.q + off)
@@ -176,20 +158,42 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
           }
         }
 #pragma unroll
-        for (int q = 0; q < P; ++q) qf[q][m][kb] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+        for (int q = 0; q < P; ++q) qf[q][kb] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
       }
     }
-
-    float o[MT][NB][4], mx[MT][2], sum[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int d = 0; d < NB; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[m][d][e] = 0.f;
-      mx[m][0] = mx[m][1] = -INFINITY;
-      sum[m][0] = sum[m][1] = 0.f;
+    for (int i = 1; i < count; i *= 2) {
+      uint64_t seen = 0;
+      int up = -1;
+      if (tid < MK_MAX_TREE) {
+        up = s_up[tid];
+        seen = s_seen[tid];
+        if (up >= 0) {
+          seen |= s_seen[up];
+          up = s_up[up];
+        }
+      }
+      __syncthreads();
+      if (tid < MK_MAX_TREE) {
+        s_up[tid] = up;
+        s_seen[tid] = seen;
+      }
+      __syncthreads();
     }
+
+    uint64_t seen[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = rt * RT + h * 8 + grp;
+      seen[h] = r < rows ? s_seen[r / p.G] : 0;
+    }
+
+    float o[NB][4], mx[2], sum[2];
+#pragma unroll
+    for (int d = 0; d < NB; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    mx[0] = mx[1] = -INFINITY;
+    sum[0] = sum[1] = 0.f;
 
     // ---- the tiles
     for (int it = 0; it < n; ++it) {
@@ -230,138 +234,136 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
         odd = __syncthreads_or(bad);
       }
 
-      // scores of the warp's 16 keys
-      float s[MT][2][4];
+      // scores of the warp's keys
+      float s[NK][2][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[m][j][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[nk][j][e] = 0.f;
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        // blocks: keys 0-7 dims 0-7, keys 0-7 dims 8-15, keys 8-15 dims 0-7, ...
-        const int r = warp * 16 + (lane / 16) * 8 + lane % 8, c = kb * 2 + (lane / 8) % 2;
-        uint32_t kf[4];
-        ldsm_x4(kf, ks + r * (D * 2) + ((c ^ (r & 7)) * 16));
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int nk = 0; nk < NK; ++nk) {
+          // blocks: keys 0-7 dims 0-7, keys 0-7 dims 8-15, keys 8-15 dims 0-7, ...
+          const int r = (warp * NK + nk) * 16 + (lane / 16) * 8 + lane % 8, c = kb * 2 + (lane / 8) % 2;
+          uint32_t kf[4];
+          ldsm_x4(kf, ks + r * (D * 2) + ((c ^ (r & 7)) * 16));
           if constexpr (P == 1) {
-            mma_bf16_16816(s[m][0], qf[0][m][kb], kf[0], kf[1]);
-            mma_bf16_16816(s[m][1], qf[0][m][kb], kf[2], kf[3]);
+            mma_bf16_16816(s[nk][0], qf[0][kb], kf[0], kf[1]);
+            mma_bf16_16816(s[nk][1], qf[0][kb], kf[2], kf[3]);
           } else {
             // the matrix unit may truncate as it accumulates: the smallest parts
             // first, and the sums over the dimensions by rounded adds
             float x[2][4] = {};
 #pragma unroll
             for (int q = P - 1; q >= 0; --q) {
-              mma_bf16_16816(x[0], qf[q][m][kb], kf[0], kf[1]);
-              mma_bf16_16816(x[1], qf[q][m][kb], kf[2], kf[3]);
+              mma_bf16_16816(x[0], qf[q][kb], kf[0], kf[1]);
+              mma_bf16_16816(x[1], qf[q][kb], kf[2], kf[3]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[m][0][e] += x[0][e], s[m][1][e] += x[1][e];
+            for (int e = 0; e < 4; ++e) s[nk][0][e] += x[0][e], s[nk][1][e] += x[1][e];
           }
         }
-      }
       // what is not seen: keys behind the length, pages that are not there,
       // nodes that are no ancestors
-      const uint32_t mine = lane < 16 ? tab[warp * 16 + lane] : 0;
+      const uint32_t mine = lane < 16 * NK ? tab[warp * 16 * NK + lane] : 0;
       const bool plain = slot0 + kTile <= start && !__any_sync(0xffffffffu, mine == kNoRow);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[m][j][e] *= p.scale_log2;
+            s[nk][j][e] *= p.scale_log2;
             if (!plain) {
-              const int key = warp * 16 + j * 8 + 2 * tig + (e & 1);
+              const int key = (warp * NK + nk) * 16 + j * 8 + 2 * tig + (e & 1);
               const int node = slot0 + key - start;
-              const bool see = tab[key] != kNoRow && (node < 0 || (seen[m][e / 2] >> node & 1));
-              if (!see) s[m][j][e] = -INFINITY;
+              const bool see = tab[key] != kNoRow && (node < 0 || (seen[e / 2] >> node & 1));
+              if (!see) s[nk][j][e] = -INFINITY;
             }
           }
 
       // running maximum and sum
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int h = 0; h < 2; ++h) {
+        float t = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float t = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]),
-                          fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1]));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-          t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-          const float now = fmaxf(mx[m][h], t);
-          const float from = now == -INFINITY ? 0.f : now;  // nothing seen yet: weights 0
-          const float keep = fast_exp2(mx[m][h] - from);
-          mx[m][h] = now;
-          float add = 0.f;
+        for (int nk = 0; nk < NK; ++nk)
+          t = fmaxf(t, fmaxf(fmaxf(s[nk][0][2 * h], s[nk][0][2 * h + 1]),
+                             fmaxf(s[nk][1][2 * h], s[nk][1][2 * h + 1])));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+        const float now = fmaxf(mx[h], t);
+        const float from = now == -INFINITY ? 0.f : now;  // nothing seen yet: weights 0
+        const float keep = fast_exp2(mx[h] - from);
+        mx[h] = now;
+        float add = 0.f;
+#pragma unroll
+        for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float w = fast_exp2(s[m][j][2 * h + e] - from);
-              s[m][j][2 * h + e] = w;
+              const float w = fast_exp2(s[nk][j][2 * h + e] - from);
+              s[nk][j][2 * h + e] = w;
               add += w;
             }
-          sum[m][h] = sum[m][h] * keep + add;
-          if (__any_sync(0xffffffffu, keep != 1.f)) {
+        sum[h] = sum[h] * keep + add;
+        if (__any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll
-            for (int d = 0; d < NB; ++d) {
-              o[m][d][2 * h] *= keep;
-              o[m][d][2 * h + 1] *= keep;
-            }
+          for (int d = 0; d < NB; ++d) {
+            o[d][2 * h] *= keep;
+            o[d][2 * h + 1] *= keep;
           }
         }
+      }
 
       // o += weights x v
-      uint4 w[P][MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t x[4][P];
+      for (int nk = 0; nk < NK; ++nk) {
+        uint4 w[P];
+        uint32_t part[4][P];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) split(s[m][j / 2][j % 2 * 2], s[m][j / 2][j % 2 * 2 + 1], x[j]);
+        for (int j = 0; j < 4; ++j)
+          split(s[nk][j / 2][j % 2 * 2], s[nk][j / 2][j % 2 * 2 + 1], part[j]);
 #pragma unroll
-        for (int q = 0; q < P; ++q) w[q][m] = make_uint4(x[0][q], x[1][q], x[2][q], x[3][q]);
-      }
+        for (int q = 0; q < P; ++q) w[q] = make_uint4(part[0][q], part[1][q], part[2][q], part[3][q]);
 #pragma unroll
-      for (int d = 0; d < NB; d += 2) {
-        const int r = warp * 16 + (lane / 8) % 2 * 8 + lane % 8, c = d + lane / 16;
-        uint32_t vf[4];
-        ldsm_x4_t(vf, vs + r * (D * 2) + ((c ^ (r & 7)) * 16));
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int d = 0; d < NB; d += 2) {
+          const int r = (warp * NK + nk) * 16 + (lane / 8) % 2 * 8 + lane % 8, c = d + lane / 16;
+          uint32_t vf[4];
+          ldsm_x4_t(vf, vs + r * (D * 2) + ((c ^ (r & 7)) * 16));
           if constexpr (P == 1) {
-            mma_bf16_16816(o[m][d], w[0][m], vf[0], vf[1]);
-            mma_bf16_16816(o[m][d + 1], w[0][m], vf[2], vf[3]);
+            mma_bf16_16816(o[d], w[0], vf[0], vf[1]);
+            mma_bf16_16816(o[d + 1], w[0], vf[2], vf[3]);
           } else {
             float x[2][4] = {};
 #pragma unroll
             for (int q = P - 1; q >= 0; --q) {
-              mma_bf16_16816(x[0], w[q][m], vf[0], vf[1]);
-              mma_bf16_16816(x[1], w[q][m], vf[2], vf[3]);
+              mma_bf16_16816(x[0], w[q], vf[0], vf[1]);
+              mma_bf16_16816(x[1], w[q], vf[2], vf[3]);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[m][d][e] += x[0][e], o[m][d + 1][e] += x[1][e];
+            for (int e = 0; e < 4; ++e) o[d][e] += x[0][e], o[d + 1][e] += x[1][e];
           }
         }
       }
       if (odd) {
 #pragma unroll 1
-        for (int key = warp * 16; key < warp * 16 + 16; ++key) {
+        for (int key = warp * 16 * NK; key < (warp + 1) * 16 * NK; ++key) {
           const int node = slot0 + key - start;
           if (node < 0 || node >= count || tab[key] == kNoRow) continue;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int d = 0; d < NB; ++d)
 #pragma unroll
-            for (int d = 0; d < NB; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int c = d * 8 + 2 * tig + (e & 1);
-                if (!(seen[m][e / 2] >> node & 1)) continue;
-                if (s_odd[node][0][c / 32] >> (c % 32) & 1) o[m][d][e] += INFINITY;
-                if (s_odd[node][1][c / 32] >> (c % 32) & 1) o[m][d][e] -= INFINITY;
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int c = d * 8 + 2 * tig + (e & 1);
+              if (!(seen[e / 2] >> node & 1)) continue;
+              if (s_odd[node][0][c / 32] >> (c % 32) & 1) o[d][e] += INFINITY;
+              if (s_odd[node][1][c / 32] >> (c % 32) & 1) o[d][e] -= INFINITY;
+            }
         }
       }
       if (tid < kTile) rowtab[(it + kStages) % (kStages + 1) * kTile + tid] = next_row;
@@ -370,31 +372,27 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
     // ---- the warps' shares joined: sums within a quad, maxima across warps
     cp_async_wait<0>();
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 1);
-        sum[m][h] += __shfl_xor_sync(0xffffffffu, sum[m][h], 2);
-        if (tig == 0) {
-          s_ml[warp][m * 16 + h * 8 + grp][0] = mx[m][h];
-          s_ml[warp][m * 16 + h * 8 + grp][1] = sum[m][h];
-        }
+    for (int h = 0; h < 2; ++h) {
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+      sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+      if (tig == 0) {
+        s_ml[warp][h * 8 + grp][0] = mx[h];
+        s_ml[warp][h * 8 + grp][1] = sum[h];
       }
+    }
     __syncthreads();  // also: everybody is done with the ring
     float* so = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int h = 0; h < 2; ++h) {
+      const int r = h * 8 + grp;
+      const float top = fmaxf(fmaxf(s_ml[0][r][0], s_ml[1][r][0]), fmaxf(s_ml[2][r][0], s_ml[3][r][0]));
+      const float f = fast_exp2(mx[h] - top);
+      const bool none = sum[h] == 0.f;  // a seen key's largest weight is 1 (or NaN)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = m * 16 + h * 8 + grp;
-        const float top = fmaxf(fmaxf(s_ml[0][r][0], s_ml[1][r][0]), fmaxf(s_ml[2][r][0], s_ml[3][r][0]));
-        const float f = fast_exp2(mx[m][h] - top);
-        const bool none = sum[m][h] == 0.f;  // a seen key's largest weight is 1 (or NaN)
-#pragma unroll
-        for (int d = 0; d < NB; ++d)
-          *reinterpret_cast<float2*>(so + (warp * RT + r) * D + d * 8 + 2 * tig) =
-              none ? make_float2(0.f, 0.f) : make_float2(o[m][d][2 * h] * f, o[m][d][2 * h + 1] * f);
-      }
+      for (int d = 0; d < NB; ++d)
+        *reinterpret_cast<float2*>(so + (warp * RT + r) * D + d * 8 + 2 * tig) =
+            none ? make_float2(0.f, 0.f) : make_float2(o[d][2 * h] * f, o[d][2 * h + 1] * f);
+    }
     __syncthreads();
     const bool whole = n == sh.nt;
     const size_t slot = part_slot(p, group, sh.begins, rt);
@@ -431,31 +429,32 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   }
 }
 
-// Joins the shares of the items that were cut. WPR warps take a row (few rows:
-// all four of the block, many: one each), each lane D / 32 of its columns. The
-// lanes read the shares' maxima and sums 32 at a time, so that every share's
-// factor is known before its columns are read; the warps of a row take the
-// shares in turn and add up in shared memory, in a fixed order.
-template <int D, int WPR, typename T>
+// Joins the shares of the items that were cut. Few rows: the four warps of a block
+// take one row, every fourth share each, and add up in shared memory in a
+// fixed order. Many: a warp takes a row (four one after another took 6 us longer
+// on 6400 rows). A lane has D / 32 of the row's columns; the lanes read the
+// shares' maxima and sums 32 at a time, so that every share's factor is known
+// before its columns are read.
+template <int D, bool FEW, typename T>
 __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32, ROWS = 4 / WPR;
+  constexpr int E = D / 32, TURNS = FEW ? 4 : 1;
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   __shared__ int prefix[kMaxSeqs + 1];
   __shared__ Vec other[4][32];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, turn = warp % WPR;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, turn = FEW ? warp : 0;
   const int b = blockIdx.y / p.cache.n_kv, g = blockIdx.y % p.cache.n_kv;
   if (warp == 0) work_line(p, prefix);
   __syncthreads();
-  const int row = blockIdx.x * ROWS + warp / WPR;
-  const int nt = (prefix[b + 1] - prefix[b]) / p.cache.n_kv;
+  const int row = FEW ? blockIdx.x : blockIdx.x * 4 + warp;
+  const int places = (prefix[b + 1] - prefix[b]) / p.cache.n_kv;
   const int rt = row / p.row_tile, r = row - rt * p.row_tile;
-  bool cut_up = nt > 0 && row < clamped(p.counts, b, p.T) * p.G;
+  bool cut_up = places > 0 && row < clamped(p.counts, b, p.T) * p.G;
   int g0 = 0, g1 = 0, item0 = 0;
   const Cut cut(prefix[p.B], p.groups);
   if (cut_up) {
-    item0 = prefix[b] + g * nt;
-    g0 = cut.group_of(item0);
-    g1 = cut.group_of(item0 + nt - 1);
+    item0 = prefix[b] + g * places;
+    g0 = cut.group_of(item0 + p.extra);
+    g1 = cut.group_of(item0 + places - 1);
     cut_up = g0 != g1;  // else it was written whole
   }
   griddep_wait();
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
       at = -1, ms = -INFINITY, ls = 0.f;
       if (s <= g1) {
         const int u0 = cut.begin(s);
-        if (u0 != cut.begin(s + 1)) {  // not one of more groups than tiles
+        if (u0 != cut.begin(s + 1)) {  // not one of more groups than places
           const int64_t x = (int64_t)part_slot(p, s, u0 >= item0, rt) * p.row_tile + r;
           const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + x);
           if (ml.y != 0.f) at = x, ms = ml.x, ls = ml.y;
@@ -492,9 +491,9 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
       l += ls * f;
       const int n = min(32, g1 - s0 + 1);
 #pragma unroll 4
-      for (int i = turn; i < n; i += WPR) {
-        const int64_t x = __shfl_sync(0xffffffffu, at, i);
-        const float w = __shfl_sync(0xffffffffu, f, i);
+      for (int k = turn; k < n; k += TURNS) {
+        const int64_t x = __shfl_sync(0xffffffffu, at, k);
+        const float w = __shfl_sync(0xffffffffu, f, k);
         if (x >= 0) {
           const Vec v = __ldcg(reinterpret_cast<const Vec*>(p.part_o + x * D) + lane);
           const float* c = reinterpret_cast<const float*>(&v);
@@ -506,7 +505,7 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
 #pragma unroll
     for (int d = 16; d; d /= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
   }
-  if constexpr (WPR > 1) {
+  if constexpr (FEW) {
     Vec v;
 #pragma unroll
     for (int e = 0; e < E; ++e) reinterpret_cast<float*>(&v)[e] = o[e];
@@ -514,8 +513,8 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
     __syncthreads();
     if (turn != 0) return;
 #pragma unroll
-    for (int w = 1; w < WPR; ++w) {
-      const Vec x = other[warp + w][lane];
+    for (int w = 1; w < 4; ++w) {
+      const Vec x = other[w][lane];
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] += reinterpret_cast<const float*>(&x)[e];
     }
@@ -535,20 +534,21 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
 
 struct Plan {
   bool tc;  // the kernel for many rows
-  int tile, row_tile, row_tiles, groups;
+  int tile, extra, row_tile, row_tiles, groups;
   size_t o_floats, ml_floats;
 };
 
-// Which kernel, and its tiles. Many rows of bf16 activations go to the
-// tensor-memory kernel: one block per SM, two streams of up to 128 rows each
-// (up to 128 rows: two streams over the same rows that take turns at the key
-// tiles). The others go to the warp-level kernel: 32 rows per tile for bf16
-// activations with more than 16 rows; fp32 ones keep three parts of every query
-// in registers, which leaves room for 16.
+// Which kernel, and its tiles. Up to 16 rows go to the warp-level kernel, whose
+// products are that size; more to the tensor-memory kernel: bf16 activations in
+// two streams of up to 128 rows each (up to 128 rows: two streams over the same
+// rows that take turns at the key tiles), fp32 ones in tiles of 128 rows.
 Plan plan_of(int T, int G, int D, int type, int n_sm) {
   Plan pl;
   const int rows = T * G;
-  pl.tc = rows > 16 || type == MK_TYPE_FP32;
+  pl.tc = rows > kRows;
+  // measured at 0 to 8: 25 nodes over 128 to 4096 keys (1B shape, 8 sequences) 32.8 us
+  // at 0, 25.2 at 2, 23.1 at 4, 24.2 at 8; the other cases within 2 % from 2 to 8
+  pl.extra = 4;
   if (pl.tc && type == MK_TYPE_FP32) {
     pl.tile = 128;
     pl.row_tile = 128;
@@ -561,8 +561,8 @@ Plan plan_of(int T, int G, int D, int type, int n_sm) {
     pl.row_tile = each <= 128 ? 128 : (each + 63) / 64 * 64;
     pl.groups = std::max(1, n_sm / pl.row_tiles);
   } else {
-    pl.tile = kTile;
-    pl.row_tile = type == MK_TYPE_BF16 && rows > 16 ? 32 : 16;
+    pl.tile = tile_keys(D);
+    pl.row_tile = kRows;
     pl.row_tiles = (rows + pl.row_tile - 1) / pl.row_tile;
     pl.groups = std::max(1, kCtasPerSm * n_sm / pl.row_tiles);
   }
@@ -584,7 +584,7 @@ int check_attention(const mk_cache* cache, int batch, int n_tokens, int n_heads,
   if (n_heads < 1 || n_heads % cache->n_kv_heads || n_heads / cache->n_kv_heads > kMaxG)
     return op_fail(MK_ERR_INVALID,
                    "n_heads must be a multiple of n_kv_heads, at most 8 heads per kv-head");
-  if ((int64_t)batch * cache->n_kv_heads * (view->capacity / kTile + 1) > INT32_MAX)
+  if ((int64_t)batch * cache->n_kv_heads * (view->capacity / 64 + 8) > INT32_MAX)
     return op_fail(MK_ERR_INVALID, "batch x n_kv_heads x capacity above 2^37");
   return MK_OK;
 }
@@ -598,10 +598,10 @@ int make_plan(const mk_cache* cache, int n_tokens, int n_heads, int type, Plan* 
   return MK_OK;
 }
 
-template <int D, int MT, int P>
+template <int D, int P>
 int launch(const AttnParams& p, cudaStream_t st) {
-  using Lay = Layout<D, MT, P>;
-  auto* fn = tree_attention_kernel<D, MT, P>;
+  using Lay = Layout<D, P>;
+  auto* fn = tree_attention_kernel<D, P>;
   static std::atomic<uint64_t> ready{0};
   if (int rc = allow_shared(ready, (const void*)fn, Lay::kBytes)) return rc;
   fn<<<p.groups * p.row_tiles, kThreads, Lay::kBytes, st>>>(p);
@@ -612,15 +612,14 @@ template <int D>
 int launch_all(const AttnParams& p, const Plan& pl, int type, cudaStream_t st) {
   int rc;
   if (pl.tc) rc = launch_tree_attention_tc(p, D, type, st);
-  else if (type == MK_TYPE_FP32) rc = launch<D, 1, 3>(p, st);
-  else if (pl.row_tile == 32) rc = launch<D, 2, 1>(p, st);
-  else rc = launch<D, 1, 1>(p, st);
+  else if (type == MK_TYPE_FP32) rc = launch<D, 3>(p, st);
+  else rc = launch<D, 1>(p, st);
   if (rc) return rc;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // four warps for a row where that still leaves few blocks per SM
+  // a block for a row where that still leaves few blocks per SM
   const bool few = (int64_t)p.T * p.G * p.B * p.cache.n_kv <= 2048;
   cfg.gridDim = dim3(few ? p.T * p.G : (p.T * p.G + 3) / 4, p.B * p.cache.n_kv);
   cfg.blockDim = dim3(128);
@@ -628,8 +627,8 @@ int launch_all(const AttnParams& p, const Plan& pl, int type, cudaStream_t st) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   auto* fn = type == MK_TYPE_FP32
-                 ? (few ? tree_attention_join<D, 4, float> : tree_attention_join<D, 1, float>)
-                 : (few ? tree_attention_join<D, 4, uint16_t> : tree_attention_join<D, 1, uint16_t>);
+                 ? (few ? tree_attention_join<D, true, float> : tree_attention_join<D, false, float>)
+                 : (few ? tree_attention_join<D, true, uint16_t> : tree_attention_join<D, false, uint16_t>);
   return op_cuda(cudaLaunchKernelEx(&cfg, fn, p), "mk_tree_attention");
 }
 
@@ -680,7 +679,7 @@ int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens,
   p.q = q, p.out = out, p.qs = q_stride, p.os = out_stride;
   p.starts = starts, p.parents = parents, p.counts = counts;
   p.B = batch, p.T = n_tokens, p.nh = n_heads, p.G = n_heads / cache->n_kv_heads;
-  p.tile = pl.tile, p.row_tile = pl.row_tile, p.row_tiles = pl.row_tiles, p.groups = pl.groups;
+  p.tile = pl.tile, p.extra = pl.extra, p.row_tile = pl.row_tile, p.row_tiles = pl.row_tiles, p.groups = pl.groups;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + pl.o_floats;

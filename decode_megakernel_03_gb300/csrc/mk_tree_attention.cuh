@@ -8,7 +8,9 @@
 // of blocks, wherever the cuts fall; the lengths are read on the device, so the
 // grid does not depend on them and a captured call stays valid. A share that
 // covers a (b, g) whole writes its rows; shares that cover a part write
-// (o, m, l) to the workspace and a second kernel joins them.
+// (o, m, l) to the workspace and a second kernel joins them. A share also costs
+// what its beginning and its end take: each (b, g) counts that many tiles more
+// on the line, or a block with many short sequences would be the last to finish.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -29,6 +31,7 @@ struct AttnParams {
   const int32_t *starts, *parents, *counts;
   int B, T, nh, G;
   int tile;                    // keys of a tile
+  int extra;                   // tiles that a share's beginning and end are worth
   int row_tile;                // rows of a row tile
   int row_tiles, groups;       // grid = groups x row_tiles, row tiles fastest
   float scale_log2;            // scale * log2(e)
@@ -37,8 +40,8 @@ struct AttnParams {
 };
 
 // ---- the line of work -----------------------------------------------------------
-// Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), their
-// tiles in order.
+// Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), each is
+// `extra` places and then its tiles in order.
 
 __device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
   const int n = clamped(p.counts, b, p.T);
@@ -46,14 +49,15 @@ __device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
   return min(clamped(p.starts, b, p.cache.capacity) + n, p.cache.capacity);
 }
 
-// Fills prefix[0..B] (tiles of the sequences before b, times n_kv) with one warp.
-// (The host makes sure that the line has fewer than 2^31 tiles.)
+// Fills prefix[0..B] (places of the sequences before b) with one warp. (The host
+// makes sure that the line has fewer than 2^31 places.)
 __device__ __forceinline__ void work_line(const AttnParams& p, int* prefix) {
   const int lane = threadIdx.x % 32;
   int sum = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int x = b < p.B ? (keys_of(p, b) + p.tile - 1) / p.tile * p.cache.n_kv : 0;
+    int x = b < p.B ? (keys_of(p, b) + p.tile - 1) / p.tile : 0;
+    if (x > 0) x = (x + p.extra) * p.cache.n_kv;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -66,7 +70,7 @@ __device__ __forceinline__ void work_line(const AttnParams& p, int* prefix) {
   __syncwarp();
 }
 
-// The cut of a line of W tiles: group s has the tiles [begin(s), begin(s + 1)),
+// The cut of a line of W places: group s has the places [begin(s), begin(s + 1)),
 // begin(s) = floor(s W / groups) = s q + floor(s r / groups).
 struct Cut {
   int W, groups, q, r;
@@ -77,7 +81,7 @@ struct Cut {
   __device__ __forceinline__ int begin(int s) const {
     return s * q + (int)((unsigned)(s * r) / (unsigned)groups);
   }
-  // the group that has tile u
+  // the group that has place u
   __device__ __forceinline__ int group_of(int u) const {
     const uint64_t x = (uint64_t)(u + 1) * groups - 1;
     return x >> 32 ? (int)(x / (unsigned)W) : (int)((unsigned)x / (unsigned)W);
@@ -92,23 +96,28 @@ struct Share {
   int count, start, len, rows;
 };
 
-// The share at tile u, which moves behind it. False at the end of the part.
+// The next share from place u on, which moves behind it. False at the end of the
+// part [u_begin, u_end).
 __device__ __forceinline__ bool next_share(const AttnParams& p, const int* prefix, int u_begin,
                                            int u_end, int& u, Share& s) {
-  if (u >= u_end) return false;
-  int lo = 0, hi = p.B;  // the last sequence whose prefix is <= u
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (prefix[mid] <= u) lo = mid;
-    else hi = mid;
-  }
-  s.b = lo;
-  s.nt = (prefix[lo + 1] - prefix[lo]) / p.cache.n_kv;
-  s.g = (u - prefix[lo]) / s.nt;
-  s.k0 = u - prefix[lo] - s.g * s.nt;
-  s.n = min(s.nt - s.k0, u_end - u);
-  s.begins = u == u_begin;
-  u += s.n;
+  do {
+    if (u >= u_end) return false;
+    int lo = 0, hi = p.B;  // the last sequence whose prefix is <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (prefix[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    const int places = (prefix[lo + 1] - prefix[lo]) / p.cache.n_kv;
+    s.b = lo;
+    s.nt = places - p.extra;
+    s.g = (u - prefix[lo]) / places;
+    const int tile0 = prefix[lo] + s.g * places + p.extra;  // place of the item's tile 0
+    s.k0 = max(u - tile0, 0);
+    s.n = min(u_end - tile0, s.nt) - s.k0;
+    s.begins = u == u_begin;
+    u = tile0 + s.nt;
+  } while (s.n <= 0);  // a part that ends before the item's first tile
   s.count = clamped(p.counts, s.b, p.T);
   s.start = clamped(p.starts, s.b, p.cache.capacity);
   s.len = min(s.start + s.count, p.cache.capacity);

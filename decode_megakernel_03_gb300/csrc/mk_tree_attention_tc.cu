@@ -102,6 +102,12 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -732,15 +738,15 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
         unsigned long long sums[2] = {0, 0};
         __syncwarp();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 a = weights2(x[64 * h + 2 * e], x[64 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
+          for (int e = 0; e < 16; ++e) {
+            const float2 a = weights2(x[32 * h + 2 * e], x[32 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
             w[e] = bf16x2_rn(a.x, a.y);
           }
-          tmem_store32(t_s + 32 * h, w);
-          if (h == 0) {  // its products need not wait for the second half
+          tmem_store16(t_s + 16 * h, w);
+          if (h == 1) {  // its products need not wait for the second half
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -785,15 +791,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
       const size_t slot = part_slot(p, group, sh.begins, rt) * p.row_tile + local;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
-        uint32_t o[32], o1[32];
-        tmem_load32(t_o + c, o);
-        if (second) tmem_load32(t_o + D + c, o1);
-        tmem_wait_ld();
+        uint32_t o[32];
         float y[32];
+        tmem_load32(t_o + c, o);
+        tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          y[e] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
-          if (second && f1 != 0.f) y[e] += __uint_as_float(o1[e]) * f1;
+        for (int e = 0; e < 32; ++e) y[e] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
+        if (second) {
+          tmem_load32(t_o + D + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] += f1 != 0.f ? __uint_as_float(o[e]) * f1 : 0.f;
         }
         put_columns<D, 1>(p, sh, sm, share, seen, row, c, live, l, slot, y);
       }
@@ -862,15 +870,15 @@ __device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, cons
           unsigned long long sums[2] = {0, 0};
           __syncwarp();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[3][16];
+          for (int h = 0; h < 4; ++h) {
+            uint32_t w[3][8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 a = weights2(x[32 * h + 2 * e], x[32 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
+            for (int e = 0; e < 8; ++e) {
+              const float2 a = weights2(x[16 * h + 2 * e], x[16 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
               split_exactly(a, w[0][e], w[1][e], w[2][e]);
             }
 #pragma unroll
-            for (int q = 0; q < 3; ++q) tmem_store16(t_s + q * 64 + 32 * half + 16 * h, w[q]);
+            for (int q = 0; q < 3; ++q) tmem_store8(t_s + q * 64 + 32 * half + 8 * h, w[q]);
           }
           add2(sums[0], sums[1]);
           const float2 sum = unpack2(sums[0]);
@@ -965,7 +973,7 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   const Cut cut(prefix[p.B], p.groups);
   const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
 
-  // Registers: 16 warps launched with 128 each, 8 x 184 + 4 x 88 + 4 x 56 is the
+  // Registers: 16 warps launched with 128 each, 8 x 184 + 8 x 72 is the
   // same sum. A row's thread holds a tile's 128 scores; the loading warps need
   // room for the addresses of the copies in flight (56 registers: 105 cycles a
   // copy, because each waited for the last one's operands to be read).
@@ -977,10 +985,10 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
       softmax_role<D, KIND>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
     }
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     load_role<D, KIND>(p, sm, prefix, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kMmaWarp)
       mma_role<D, KIND>(p, sm, prefix, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
   }

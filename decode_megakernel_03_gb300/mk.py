@@ -527,38 +527,23 @@ class Rope:
         _check(lib().mk_rope_init(ctypes.byref(cfg), self.ref))
 
 
-# the current stream's handle without making a Stream object (a few microseconds
-# less per call), where this torch has it
+# the current stream's handle and device without making objects (a few
+# microseconds less per call), where this torch has the short ways
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-class _Call:
-    """The launch context of a call on `device`: its raw stream, the device made
-    current, new tensors that belong to the stream."""
-
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise _bad("stream and tensors are on different devices")
-        self.device, self.stream, self.guards = device, stream, None
-        self.raw = _current_raw(device.index) if stream is None else stream.cuda_stream
-
-    def __enter__(self):
-        if self.stream is not None or torch.cuda.current_device() != self.device.index:
-            self.guards = [torch.cuda.device(self.device)]
-            if self.stream is not None:
-                self.guards.append(torch.cuda.stream(self.stream))
-            for g in self.guards:
-                g.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guards:
-            for g in reversed(self.guards):
-                g.__exit__(*exc)
-
-    def new(self, shape, dtype, zero=False):
-        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self.device)
+def _elsewhere(device, stream):
+    """None where a call on `device` can launch at once on the current stream;
+    else a context that makes the device (and the stream) current, inside which
+    the call starts again: its launch, and the tensors that it allocates,
+    belong to that stream then."""
+    if stream is None:
+        return None if _current_device() == device.index else torch.cuda.device(device)
+    if stream.device != device:
+        raise _bad("stream and tensors are on different devices")
+    return torch.cuda.stream(stream)
 
 
 def _ints(t, device, what: str, shape):
@@ -606,6 +591,10 @@ def _heads(t, shape, dtype, device, what: str) -> int:
     return sn
 
 
+def _new(shape, dtype, device, zero: bool):
+    return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
+
+
 def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=None, counts=None,
                 q_out=None, stream=None):
     """mk_rope_append: q [B][T][nh][D], k, v [B][T][nkv][D] (bf16 or fp32; views
@@ -613,20 +602,22 @@ def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=N
     counts [B] int32, all on the device. Returns the rotated queries (q_out,
     which may be q; else a new tensor, whose rows behind counts are 0)."""
     dev = cache.device
+    if (other := _elsewhere(dev, stream)) is not None:
+        with other:
+            return rope_append(rope, cache, layer, q, k, v, starts, parents, counts, q_out)
     shape, kind, qs = _queries(q, cache)
     b, n, nh, d = shape
     kv, dtype = (b, n, cache.n_kv_heads, d), q.dtype
     ks, vs = _heads(k, kv, dtype, dev, "k"), _heads(v, kv, dtype, dev, "v")
     sp = _ints(starts, dev, "starts", (b,))
     pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
-    with _Call(dev, stream) as call:
-        if q_out is None:
-            q_out, os_ = call.new(shape, dtype, counts is not None), nh * d
-        else:
-            os_ = _heads(q_out, shape, dtype, dev, "q_out")
-        _check(lib().mk_rope_append(rope.ref, cache.ref, layer, b, n, nh, kind, q.data_ptr(), qs,
-                                    k.data_ptr(), ks, v.data_ptr(), vs, q_out.data_ptr(), os_, sp,
-                                    pp, cp, call.raw))
+    if q_out is None:
+        q_out, os_ = _new(shape, dtype, dev, counts is not None), nh * d
+    else:
+        os_ = _heads(q_out, shape, dtype, dev, "q_out")
+    _check(lib().mk_rope_append(rope.ref, cache.ref, layer, b, n, nh, kind, q.data_ptr(), qs,
+                                k.data_ptr(), ks, v.data_ptr(), vs, q_out.data_ptr(), os_, sp, pp,
+                                cp, _current_raw(dev.index)))
     return q_out
 
 
@@ -637,24 +628,27 @@ def tree_attention(cache: Cache, layer: int, q, starts, parents=None, counts=Non
     1 / sqrt(D). Returns out (given, or new; new rows behind counts are 0). The
     workspace is allocated for the call on its stream."""
     dev = cache.device
+    if (other := _elsewhere(dev, stream)) is not None:
+        with other:
+            return tree_attention(cache, layer, q, starts, parents, counts, scale, out)
     shape, kind, qs = _queries(q, cache)
     b, n, nh, d = shape
     sp = _ints(starts, dev, "starts", (b,))
     pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
     size = cache.workspaces.get((b, n, nh, kind))
-    with _Call(dev, stream) as call:
-        if size is None:
-            need = ctypes.c_size_t()
-            _check(lib().mk_tree_attention_workspace(cache.ref, b, n, nh, kind, ctypes.byref(need)))
-            size = cache.workspaces[b, n, nh, kind] = need.value
-        ws = call.new(size, torch.uint8)
-        if out is None:
-            out, os_ = call.new(shape, q.dtype, counts is not None), nh * d
-        else:
-            os_ = _heads(out, shape, q.dtype, dev, "out")
-        _check(lib().mk_tree_attention(cache.ref, layer, b, n, nh, kind,
-                                       d ** -0.5 if scale is None else scale, q.data_ptr(), qs, sp,
-                                       pp, cp, out.data_ptr(), os_, ws.data_ptr(), size, call.raw))
+    if size is None:
+        need = ctypes.c_size_t()
+        _check(lib().mk_tree_attention_workspace(cache.ref, b, n, nh, kind, ctypes.byref(need)))
+        size = cache.workspaces[b, n, nh, kind] = need.value
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    if out is None:
+        out, os_ = _new(shape, q.dtype, dev, counts is not None), nh * d
+    else:
+        os_ = _heads(out, shape, q.dtype, dev, "out")
+    _check(lib().mk_tree_attention(cache.ref, layer, b, n, nh, kind,
+                                   d ** -0.5 if scale is None else scale, q.data_ptr(), qs, sp, pp,
+                                   cp, out.data_ptr(), os_, ws.data_ptr(), size,
+                                   _current_raw(dev.index)))
     return out
 
 
@@ -664,6 +658,9 @@ def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     dev, shape = logits.device, logits.shape
     if not logits.is_cuda or len(shape) != 3:
         raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
+    if (other := _elsewhere(dev, stream)) is not None:
+        with other:
+            return tree_accept(logits, tokens, parents, counts)
     kind = _type_of(logits, "logits")
     b, n, vocab = shape
     sb, sn, sv = logits.stride()
@@ -674,15 +671,14 @@ def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
     need = ctypes.c_size_t()
     _check(lib().mk_tree_accept_workspace(b, n, vocab, ctypes.byref(need)))
-    # one allocation: the workspace (a few KB), then the outputs behind it
+    # one allocation: the workspace (tens of KB), then the outputs behind it
     first, rows = -(-need.value // 4), b * n
-    with _Call(dev, stream) as call:
-        buf = call.new(first + 2 * rows + 2 * b, torch.int32)
-        ws = buf.data_ptr()
-        at = ws + 4 * first
-        _check(lib().mk_tree_accept(b, n, vocab, kind, logits.data_ptr(), stride, tp, pp, cp, at,
-                                    at + 4 * rows, at + 8 * rows, at + 8 * rows + 4 * b, ws,
-                                    need.value, call.raw))
+    buf = torch.empty(first + 2 * rows + 2 * b, dtype=torch.int32, device=dev)
+    ws = buf.data_ptr()
+    at = ws + 4 * first
+    _check(lib().mk_tree_accept(b, n, vocab, kind, logits.data_ptr(), stride, tp, pp, cp, at,
+                                at + 4 * rows, at + 8 * rows, at + 8 * rows + 4 * b, ws,
+                                need.value, _current_raw(dev.index)))
     last = first + 2 * rows
     return (buf.as_strided((b, n), (n, 1), first), buf.as_strided((b, n), (n, 1), first + rows),
             buf.as_strided((b,), (1,), last), buf.as_strided((b,), (1,), last + b))
@@ -693,13 +689,15 @@ def cache_compact(cache: Cache, starts, path, accepted, stream=None):
     in every layer; starts [B], path [B][T], accepted [B] as tree_accept gives
     them."""
     dev = cache.device
+    if (other := _elsewhere(dev, stream)) is not None:
+        with other:
+            return cache_compact(cache, starts, path, accepted)
     if len(path.shape) != 2:
         raise _bad("path must be [batch][tokens]")
     b, n = path.shape
     sp = _ints(starts, dev, "starts", (b,))
     pp, ap = _ints(path, dev, "path", (b, n)), _ints(accepted, dev, "accepted", (b,))
-    with _Call(dev, stream) as call:
-        _check(lib().mk_cache_compact(cache.ref, b, n, sp, pp, ap, call.raw))
+    _check(lib().mk_cache_compact(cache.ref, b, n, sp, pp, ap, _current_raw(dev.index)))
 
 
 def _host_ints(x) -> np.ndarray:
@@ -719,11 +717,14 @@ def _at(a: np.ndarray) -> int:
 def cache_copy_blocks(cache: Cache, copies, stream=None):
     """mk_cache_copy_blocks: copies [n][3] on the host, (src, dst, rows) each, as
     the calls of Pages return them."""
+    if (other := _elsewhere(cache.device, stream)) is not None:
+        with other:
+            return cache_copy_blocks(cache, copies)
     c = _host_ints(copies)
     if c.size and (c.ndim != 2 or c.shape[1] != 3):
         raise _bad("copies must be [n][3]")
-    with _Call(cache.device, stream) as call:
-        _check(lib().mk_cache_copy_blocks(cache.ref, _at(c), c.size // 3, call.raw))
+    _check(lib().mk_cache_copy_blocks(cache.ref, _at(c), c.size // 3,
+                                      _current_raw(cache.device.index)))
 
 
 class Pages:
