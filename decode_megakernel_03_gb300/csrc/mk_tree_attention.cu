@@ -56,7 +56,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   constexpr int NK = kTile / 64;  // blocks of 16 keys that a warp takes of a tile
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t* rowtab = reinterpret_cast<uint32_t*>(smem + Lay::kRing);  // [kStages + 1][kTile]
-  __shared__ int prefix[kMaxSeqs + 1];
+  __shared__ Line line;
   __shared__ uint64_t s_seen[MK_MAX_TREE];   // node -> the nodes it sees
   __shared__ int s_up[MK_MAX_TREE];
   // non-finite values of the nodes' v rows: bit d % 32 of word d / 32, +inf in
@@ -69,14 +69,14 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   const uint32_t ring = smem_u32(smem);
 
   griddep_launch();
-  if (warp == 0) work_line(p, prefix);
+  if (warp == 0) work_line(p, line);
   __syncthreads();
-  const Cut cut(prefix[p.B], p.groups);
+  const Cut cut(line.prefix[p.B], p.groups);
   const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
   int u = u_begin;
 
   Share sh;
-  while (next_share(p, prefix, u_begin, u_end, u, sh)) {
+  while (next_share(p, line, u_begin, u_end, u, sh)) {
     const int b = sh.b, g = sh.g, k0 = sh.k0, n = sh.n;
     const int count = sh.count, start = sh.start, len = sh.len, rows = sh.rows;
     if (rt * RT >= rows) continue;  // no row of this tile is there
@@ -437,22 +437,22 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
 // before its columns are read.
 template <int D, bool FEW, typename T>
 __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32, TURNS = FEW ? 4 : 1;
+  constexpr int E = D / 32, TURNS = FEW ? 4 : 1, U = FEW ? 8 : 2;  // U: loads in flight
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
-  __shared__ int prefix[kMaxSeqs + 1];
+  __shared__ Line line;
   __shared__ Vec other[4][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, turn = FEW ? warp : 0;
   const int b = blockIdx.y / p.cache.n_kv, g = blockIdx.y % p.cache.n_kv;
-  if (warp == 0) work_line(p, prefix);
+  if (warp == 0) work_line(p, line);
   __syncthreads();
   const int row = FEW ? blockIdx.x : blockIdx.x * 4 + warp;
-  const int places = (prefix[b + 1] - prefix[b]) / p.cache.n_kv;
+  const int places = (line.prefix[b + 1] - line.prefix[b]) / p.cache.n_kv;
   const int rt = row / p.row_tile, r = row - rt * p.row_tile;
-  bool cut_up = places > 0 && row < clamped(p.counts, b, p.T) * p.G;
+  bool cut_up = places > 0 && row < line.count[b] * p.G;
   int g0 = 0, g1 = 0, item0 = 0;
-  const Cut cut(prefix[p.B], p.groups);
+  const Cut cut(line.prefix[p.B], p.groups);
   if (cut_up) {
-    item0 = prefix[b] + g * places;
+    item0 = line.prefix[b] + g * places;
     g0 = cut.group_of(item0 + p.extra);
     g1 = cut.group_of(item0 + places - 1);
     cut_up = g0 != g1;  // else it was written whole
@@ -490,15 +490,23 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
       const float f = at < 0 ? 0.f : fast_exp2(ms - m);
       l += ls * f;
       const int n = min(32, g1 - s0 + 1);
-#pragma unroll 4
-      for (int k = turn; k < n; k += TURNS) {
-        const int64_t x = __shfl_sync(0xffffffffu, at, k);
-        const float w = __shfl_sync(0xffffffffu, f, k);
-        if (x >= 0) {
-          const Vec v = __ldcg(reinterpret_cast<const Vec*>(p.part_o + x * D) + lane);
-          const float* c = reinterpret_cast<const float*>(&v);
+      for (int k0 = turn; k0 < n; k0 += U * TURNS) {
+        Vec v[U];
+        float w[U];
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += c[e] * w;
+        for (int i = 0; i < U; ++i) {
+          const int k = k0 + i * TURNS;
+          const int64_t x = __shfl_sync(0xffffffffu, at, k & 31);
+          w[i] = __shfl_sync(0xffffffffu, f, k & 31);
+          v[i] = Vec{};
+          if (k < n && x >= 0) v[i] = __ldcg(reinterpret_cast<const Vec*>(p.part_o + x * D) + lane);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float* c = reinterpret_cast<const float*>(&v[i]);
+          const bool has = k0 + i * TURNS < n;
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += has ? c[e] * w[i] : 0.f;
         }
       }
     }

@@ -43,30 +43,39 @@ struct AttnParams {
 // Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), each is
 // `extra` places and then its tiles in order.
 
-__device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
-  const int n = clamped(p.counts, b, p.T);
-  if (n == 0) return 0;
-  return min(clamped(p.starts, b, p.cache.capacity) + n, p.cache.capacity);
-}
 
-// Fills prefix[0..B] (places of the sequences before b) with one warp. (The host
-// makes sure that the line has fewer than 2^31 places.)
-__device__ __forceinline__ void work_line(const AttnParams& p, int* prefix) {
+// The line in shared memory: the places of the sequences before b, and the
+// sequences' starts and counts (at their bounds).
+struct Line {
+  int prefix[kMaxSeqs + 1];
+  int start[kMaxSeqs];
+  uint8_t count[kMaxSeqs];
+};
+
+// Fills it with one warp. (The host makes sure that the line has fewer than 2^31
+// places.)
+__device__ __forceinline__ void work_line(const AttnParams& p, Line& line) {
   const int lane = threadIdx.x % 32;
   int sum = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    int x = b < p.B ? (keys_of(p, b) + p.tile - 1) / p.tile : 0;
-    if (x > 0) x = (x + p.extra) * p.cache.n_kv;
+    int x = 0;
+    if (b < p.B) {
+      const int start = clamped(p.starts, b, p.cache.capacity), count = clamped(p.counts, b, p.T);
+      line.start[b] = start;
+      line.count[b] = (uint8_t)count;
+      const int keys = count > 0 ? min(start + count, p.cache.capacity) : 0;
+      if (keys > 0) x = ((keys + p.tile - 1) / p.tile + p.extra) * p.cache.n_kv;
+    }
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int y = __shfl_up_sync(0xffffffffu, x, d);
       if (lane >= d) x += y;
     }
-    if (b < p.B) prefix[b + 1] = sum + x;
+    if (b < p.B) line.prefix[b + 1] = sum + x;
     sum += __shfl_sync(0xffffffffu, x, 31);
   }
-  if (lane == 0) prefix[0] = 0;
+  if (lane == 0) line.prefix[0] = 0;
   __syncwarp();
 }
 
@@ -98,28 +107,28 @@ struct Share {
 
 // The next share from place u on, which moves behind it. False at the end of the
 // part [u_begin, u_end).
-__device__ __forceinline__ bool next_share(const AttnParams& p, const int* prefix, int u_begin,
+__device__ __forceinline__ bool next_share(const AttnParams& p, const Line& line, int u_begin,
                                            int u_end, int& u, Share& s) {
   do {
     if (u >= u_end) return false;
     int lo = 0, hi = p.B;  // the last sequence whose prefix is <= u
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (prefix[mid] <= u) lo = mid;
+      if (line.prefix[mid] <= u) lo = mid;
       else hi = mid;
     }
-    const int places = (prefix[lo + 1] - prefix[lo]) / p.cache.n_kv;
+    const int places = (line.prefix[lo + 1] - line.prefix[lo]) / p.cache.n_kv;
     s.b = lo;
     s.nt = places - p.extra;
-    s.g = (u - prefix[lo]) / places;
-    const int tile0 = prefix[lo] + s.g * places + p.extra;  // place of the item's tile 0
+    s.g = (u - line.prefix[lo]) / places;
+    const int tile0 = line.prefix[lo] + s.g * places + p.extra;  // place of the item's tile 0
     s.k0 = max(u - tile0, 0);
     s.n = min(u_end - tile0, s.nt) - s.k0;
     s.begins = u == u_begin;
     u = tile0 + s.nt;
   } while (s.n <= 0);  // a part that ends before the item's first tile
-  s.count = clamped(p.counts, s.b, p.T);
-  s.start = clamped(p.starts, s.b, p.cache.capacity);
+  s.count = line.count[s.b];
+  s.start = line.start[s.b];
   s.len = min(s.start + s.count, p.cache.capacity);
   s.rows = s.count * p.G;
   return true;

@@ -236,7 +236,7 @@ struct Waiter {
 // Warp w of the four takes a quarter of every tile's keys: lane i finds the row of
 // the quarter's key i, the copies take it by a shuffle.
 template <int D, int KIND>
-__device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const int* prefix,
+__device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const Line& line,
                                           uint32_t ring, uint8_t* ring_ptr, int u_begin, int u_end,
                                           int rt) {
   using Lay = Layout<D, KIND>;
@@ -251,7 +251,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
   uint32_t tile_no = 0;                  // K tiles loaded so far
   int u = u_begin;
   Share sh;
-  for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
+  for (uint32_t share = 0; next_share(p, line, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
     auto row_of = [&](int t) -> uint32_t {
       const int slot = (sh.k0 + t) * kKeys + lw * kLoadRows + lane;
@@ -352,7 +352,7 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
 // The whole warp runs the loops and waits; one elected thread issues.
 
 template <int D, int KIND>
-__device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const int* prefix,
+__device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const Line& line,
                                          uint32_t q_smem, uint32_t ring, uint32_t tmem, int u_begin,
                                          int u_end, int rt) {
   using Lay = Layout<D, KIND>;
@@ -420,7 +420,7 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
     if (++buf == Lay::kBufs) buf = 0, ++round;
     return at;
   };
-  for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
+  for (uint32_t share = 0; next_share(p, line, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
     wait(&sm.q_full, share);
     fence_async_smem();
@@ -684,7 +684,7 @@ __device__ __forceinline__ bool wait_failed(Shared& sm) {
 
 // kOne, kTwo: softmax of a stream.
 template <int D, int KIND>
-__device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, const int* prefix,
+__device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, const Line& line,
                                              uint8_t* q_ptr, uint32_t tmem, int u_begin,
                                              int u_end, int rt, int group) {
   using Lay = Layout<D, KIND>;
@@ -701,7 +701,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
   uint32_t s_uses = 0, tile_no = 0;
   int u = u_begin;
   Share sh;
-  for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
+  for (uint32_t share = 0; next_share(p, line, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
     const int row = rt * p.row_tile + local;
     const bool live = r < block_rows && row < sh.rows;
@@ -820,7 +820,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
 // memory) and keeps half of the row's output columns in registers, to which it
 // adds a tile's product while the next one is made.
 template <int D>
-__device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, const int* prefix,
+__device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, const Line& line,
                                            uint8_t* q_ptr, uint32_t tmem, int u_begin, int u_end,
                                            int rt, int group) {
   using Lay = Layout<D, kExact>;
@@ -832,7 +832,7 @@ __device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, cons
   uint32_t s_uses[2] = {0, 0}, tile_no = 0;
   int u = u_begin;
   Share sh;
-  for (uint32_t share = 0; next_share(p, prefix, u_begin, u_end, u, sh);) {
+  for (uint32_t share = 0; next_share(p, line, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
     const int row = rt * p.row_tile + r;
     const bool live = row < sh.rows, warp_live = __any_sync(0xffffffffu, live);
@@ -937,14 +937,14 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   using Lay = Layout<D, KIND>;
   extern __shared__ uint8_t raw[];
   __shared__ Shared sm;
-  __shared__ int prefix[kMaxSeqs + 1];
+  __shared__ Line line;
   const int warp = threadIdx.x / 32;
   const int rt = blockIdx.x % p.row_tiles, group = blockIdx.x / p.row_tiles;
   uint8_t* base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   uint8_t* ring_ptr = base + Lay::kQ;
 
   griddep_launch();
-  if (warp == 0) work_line(p, prefix);
+  if (warp == 0) work_line(p, line);
   if (warp == 1 && threadIdx.x % 32 == 0) {
     for (int i = 0; i < Lay::kBufs; ++i) {
       mbar_init(&sm.full[i], 32 * kLoadWarps + kLoadWarps);
@@ -970,7 +970,7 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const Cut cut(prefix[p.B], p.groups);
+  const Cut cut(line.prefix[p.B], p.groups);
   const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
 
   // Registers: 16 warps launched with 128 each, 8 x 184 + 8 x 72 is the
@@ -980,17 +980,17 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     if constexpr (KIND == kExact) {
-      exact_role<D>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
+      exact_role<D>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
     } else {
-      softmax_role<D, KIND>(p, sm, prefix, base, tmem, u_begin, u_end, rt, group);
+      softmax_role<D, KIND>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
     }
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    load_role<D, KIND>(p, sm, prefix, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
+    load_role<D, KIND>(p, sm, line, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kMmaWarp)
-      mma_role<D, KIND>(p, sm, prefix, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
+      mma_role<D, KIND>(p, sm, line, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
   }
   tc_fence_before();
   __syncthreads();
