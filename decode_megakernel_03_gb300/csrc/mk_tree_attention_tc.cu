@@ -1,5 +1,5 @@
 // Attention of a tree of drafted tokens (include/mk.h, mk_tree_attention): the
-// kernel for many rows of bf16 activations, on the tensor-memory matrix unit.
+// kernel for many rows, on the tensor-memory matrix unit.
 //
 // One block per SM, sixteen warps in warpgroups of four:
 //   warps 0-3, 4-7  softmax of stream 0 and 1, one thread per row; fp32: of
@@ -349,7 +349,11 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
 }
 
 // ---- the issuing warp ------------------------------------------------------------------
-// The whole warp runs the loops and waits; one elected thread issues.
+// The whole warp runs the loops and waits; one elected thread issues. (Issued from
+// a branch on the thread's number a product took about 100 cycles, its operands
+// being moved to uniform registers one by one; so it takes the 64 of the unit.)
+// Products run in the order of their issue, so the scores of a stream's next tile
+// may be issued over the weights that its last products read.
 
 template <int D, int KIND>
 __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const Line& line,
@@ -404,7 +408,7 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
           if (free) tc_commit(&sm.empty[at]);
           if (KIND == kExact) {
             tc_commit(&sm.t_full);
-            mbar_arrive(&sm.t_full);  // hands on the tile's factors and odd values
+            mbar_arrive(&sm.t_full);  // hands on the tile's odd values
           }
         }
       }
@@ -412,7 +416,8 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
     }
     ++p_uses[s];
   };
-  // waits for the next buffer of the ring and moves behind it
+  // Waits for the next buffer of the ring and moves behind it. The copies wrote it
+  // through the generic proxy, the products read it through the asynchronous one.
   auto take = [&]() -> uint32_t {
     wait(&sm.full[buf], round);
     fence_async_smem();

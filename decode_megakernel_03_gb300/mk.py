@@ -479,15 +479,16 @@ class Cache:
         k, v = list(k), list(v)
         if not k or len(k) != len(v):
             raise _bad("k and v must hold a tensor for each layer")
-        first = k[0]
+        shape, device = k[0].shape, k[0].device
+        if device.type != "cuda" or len(shape) != 4:
+            raise _bad("k and v must be CUDA tensors [blocks][nkv][block_size][D]")
         for t in k + v:
-            if not t.is_cuda or t.dtype != torch.bfloat16 or not t.is_contiguous():
-                raise _bad("k and v must be contiguous CUDA bfloat16 tensors")
-            if t.dim() != 4 or t.shape != first.shape or t.device != first.device:
-                raise _bad("k and v must be [blocks][nkv][block_size][D], alike in every layer")
+            if (t.dtype != torch.bfloat16 or t.shape != shape or t.device != device
+                    or not t.is_contiguous()):
+                raise _bad("k and v must be contiguous bfloat16 tensors, alike in every layer")
         self.n_layers = len(k)
-        self.n_blocks, self.n_kv_heads, self.block_size, self.head_dim = map(int, first.shape)
-        self.device = first.device
+        self.n_blocks, self.n_kv_heads, self.block_size, self.head_dim = map(int, shape)
+        self.device = device
         self.batch, entries, ptr = self.n_blocks, 0, None
         if block_table is not None:
             if len(block_table.shape) != 2:

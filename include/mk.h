@@ -432,7 +432,8 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
    ([n_heads][head_dim]); n_heads a multiple of n_kv_heads, at most 8 query
    heads per kv-head; n_tokens 1 to MK_MAX_TREE. Softmax of scale * (q . k) in
    fp32. A row that sees no key is 0; NaN and infinities in rows it does not
-   see do not reach it. Deterministic: the same inputs give the same bits.
+   see do not reach it. out may be q (with q's stride). Deterministic: the same
+   inputs give the same bits.
    Errors: MK_ERR_INVALID (also a workspace below the query's size),
    MK_ERR_CUDA. */
 int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,

@@ -66,10 +66,13 @@ def attention_bound(want, a, e, n_keys, d, dtype):
 
 
 def check_attention(rng, B, T, nh, nkv, D, dtype, bs, starts, counts=None, parents="tree", missing=0,
-                    scale=None, room=None, strided=False, poison=False):
+                    scale=None, room=None, strided=False, poison=False, ramp=0.0):
     starts = np.asarray(starts)
     room = room or int(max(starts)) + T
     k, v, table = make_cache(rng, B, room, nkv, D, bs, missing=missing)
+    if ramp:  # keys of very unlike sizes: the running maximum moves often and far
+        f = 1 + ramp * torch.rand(k[0].shape[:3], device=dev(), generator=torch.Generator(dev()).manual_seed(5))
+        k[0] = (k[0].float() * f[..., None] ** 2).to(BF16)
     par = None if parents is None else make_parents(rng, B, T, parents)
     cap = table.shape[1] * bs if bs else room
     kp, vp = host(k[0]), host(v[0])
@@ -177,6 +180,64 @@ def test_attention_missing_pages(T, dtype):
 def test_attention_scale(scale):
     rng = np.random.default_rng(1)
     check_attention(rng, 2, 6, 4, 2, 64, FP32, 16, [200, 30], scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T,nh,nkv", [(3, 4, 2), (20, 4, 2), (64, 8, 1)])
+def test_attention_scores_of_all_sizes(T, nh, nkv, dtype):
+    rng = np.random.default_rng(T)
+    check_attention(rng, 2, T, nh, nkv, 64, dtype, 16, [900, 130], ramp=3.0)
+    check_attention(rng, 2, T, nh, nkv, 128, dtype, 16, [900, 130], ramp=6.0, scale=0.7)
+
+
+@pytest.mark.parametrize("T", [2, 30, 64])
+def test_attention_in_place(T):
+    """The output over the queries: every row of q is read before it is written."""
+    rng = np.random.default_rng(T)
+    k, v, table = make_cache(rng, 3, 400, 2, 64, 16)
+    starts, cache = ints([300, 7, 90]), mk.Cache(k, v, ints(table))
+    for dtype in (BF16, FP32):
+        q = torch.randn((3, T, 16, 64), device=dev()).to(dtype)
+        want = mk.tree_attention(cache, 0, q, starts)
+        assert mk.tree_attention(cache, 0, q, starts, out=q) is q
+        assert torch.equal(q, want)
+
+
+def test_pools_of_more_than_2_to_the_31_elements():
+    """Blocks whose offsets pass 32 bits: attention, append, rows moved, pages
+    copied, against a small pool that holds the same pages."""
+    nkv, bs, D, blocks = 8, 64, 128, 36000
+    assert blocks * nkv * bs * D > 2**31
+    big = [torch.empty((blocks, nkv, bs, D), dtype=BF16, device=dev()) for _ in range(2)]
+    rng = np.random.default_rng(0)
+    table = np.stack([rng.permutation(np.arange(blocks - 60, blocks))[:10],
+                      rng.permutation(np.arange(33000, 33060))[:10]]).astype(np.int32)
+    small_table = np.arange(20, dtype=np.int32).reshape(2, 10)
+    at = torch.tensor(table.ravel(), device=dev(), dtype=torch.int64)
+    small = [torch.randn((21, nkv, bs, D), device=dev()).to(BF16) for _ in range(2)]
+    for b, s in zip(big, small):
+        b[at] = s[:20]
+    cb, cs = mk.Cache([big[0]], [big[1]], ints(table)), mk.Cache([small[0]], [small[1]], ints(small_table))
+    starts, par = ints([500, 77]), ints(make_parents(rng, 2, 40))
+
+    def same():
+        assert all(torch.equal(b[at], s[:20]) for b, s in zip(big, small))
+
+    for dtype, T in ((BF16, 2), (BF16, 40), (FP32, 2), (FP32, 40)):
+        q = torch.randn((2, T, 16, D), device=dev()).to(dtype)
+        kn, vn = (torch.randn((2, T, nkv, D), device=dev()).to(dtype) for _ in range(2))
+        p = par[:, :T].contiguous()
+        outs = [mk.tree_attention(c, 0, mk.rope_append(mk.Rope(D), c, 0, q, kn, vn, starts, p), starts, p)
+                for c in (cb, cs)]
+        assert torch.equal(*outs)
+        same()
+    path = ints([[0, 3, 7, 30] + [-1] * 36, [0, 1, 2, 39] + [-1] * 36])
+    for c in (cb, cs):
+        mk.cache_compact(c, starts, path, ints([4, 4]))
+    same()
+    mk.cache_copy_blocks(cb, [[int(table[0, 3]), 35999 if 35999 not in table else 32990, bs]])
+    dst = 35999 if 35999 not in table else 32990
+    assert torch.equal(big[0][dst], small[0][3]) and torch.equal(big[1][dst], small[1][3])
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
