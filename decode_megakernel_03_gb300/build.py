@@ -13,19 +13,21 @@ import subprocess
 import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-CSRC = os.path.join(HERE, "csrc")
+CSRC = os.path.join(HERE, "csrc")  # the decode kernel, its scheduler and ABI
+OPS = os.path.join(HERE, "ops")    # the operators over a KV cache
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libmk.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
-SOURCES = ["mk_kernel.cu", "mk_kernel_fixed_a.cu", "mk_kernel_fixed_b.cu", "mk_kernel_fx.cu",
-           "mk_kernel_dyn.cu",
-           "mk_abi.cu", "mk_sched.cpp",
-           "mk_noalloc.cu", "mk_cache_ops.cu", "mk_tree_attention.cu",
-           "mk_tree_attention_tc.cu", "mk_tree_accept.cu",
-           "mk_pages.cpp"]
+SOURCES = [os.path.join(CSRC, f) for f in (
+    "mk_kernel.cu", "mk_kernel_fixed_a.cu", "mk_kernel_fixed_b.cu", "mk_kernel_fx.cu",
+    "mk_kernel_dyn.cu", "mk_abi.cu", "mk_sched.cpp", "mk_noalloc.cu")] + [
+    os.path.join(OPS, f) for f in (
+        "mk_cache_ops.cu", "mk_tree_attention.cu", "mk_tree_attention_tc.cu", "mk_tree_accept.cu",
+        "mk_pages.cpp")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
+COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
+          "-I", CSRC, "-I", OPS]
 
 
 def _nvcc() -> str:
@@ -36,7 +38,7 @@ def _nvcc() -> str:
 
 
 def _sources_mtime() -> float:
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    paths = [os.path.join(d, f) for d in (CSRC, OPS) for f in os.listdir(d)]
     paths.append(os.path.join(ROOT, "include", "mk.h"))
     paths.append(__file__)
     return max(os.path.getmtime(p) for p in paths)
@@ -50,10 +52,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list | None =
     extra = list(extra_flags or [])
 
     def compile_one(src: str) -> str:
-        obj = os.path.join(BUILD_DIR, src + ".o")
-        cmd = [nvcc, *ARCH, *COMMON, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+        cmd = [nvcc, *ARCH, *COMMON, *extra, "-c", src, "-o", obj]
         if src.endswith(".cpp"):
-            cmd = [nvcc, *COMMON, *extra, "-x", "c++", "-c", os.path.join(CSRC, src), "-o", obj]
+            cmd = [nvcc, *COMMON, *extra, "-x", "c++", "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
