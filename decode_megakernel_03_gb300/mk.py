@@ -731,8 +731,8 @@ def cache_copy_blocks(cache: Cache, copies, stream=None):
 class Pages:
     """The page tables of a paged cache, on the host (mk_pages_*): which blocks
     each of n_seqs sequences holds. resize and compact return the copies
-    ([n][3] int32) that cache_copy_blocks has to make before the pages are
-    written; table() is what Decoder.step_paged takes."""
+    ([n][3] int32) that cache_copy_blocks has to make, one call for each result
+    and in order, before the pages are written; table() is what Decoder.step_paged takes."""
 
     def __init__(self, n_blocks: int, block_size: int, n_seqs: int, kv_capacity: int):
         self.h = ctypes.c_void_p()

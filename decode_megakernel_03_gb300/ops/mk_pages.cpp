@@ -17,6 +17,9 @@ struct mk_pages {
   std::vector<int32_t> table;    // [n_seqs][entries], -1: none
   std::vector<int32_t> length;   // [n_seqs]
   std::vector<uint64_t> free_bits;  // bit set: the page is free
+  // within mk_pages_resize: a copy of the call reads the page, so that it is not
+  // free before the call is over (a copy into it could run first)
+  std::vector<uint8_t> held;     // [n_blocks]
   int n_free = 0;
   int first = 0;                 // no free page lies in a word below this one
 
@@ -32,10 +35,21 @@ struct mk_pages {
     return b;
   }
   void give(int b) {
-    if (--refs[b] == 0) {
+    if (--refs[b] == 0 && !held[b]) {
       free_bits[b / 64] |= 1ull << (b % 64);
       first = std::min(first, b / 64);
       ++n_free;
+    }
+  }
+  // the pages that the call's copies read, free now if nobody holds them
+  void release(const std::vector<int32_t>& sources) {
+    for (int32_t b : sources) {
+      if (!held[b]) continue;  // a second copy of the same page
+      held[b] = 0;
+      if (refs[b] == 0) {
+        refs[b] = 1;
+        give(b);
+      }
     }
   }
 };
@@ -59,6 +73,7 @@ int mk_pages_create(int n_blocks, int block_size, int n_seqs, int kv_capacity, m
     p->capacity = kv_capacity;
     p->entries = p->used(kv_capacity);
     p->refs.assign(n_blocks, 0);
+    p->held.assign(n_blocks, 0);
     p->table.assign((size_t)n_seqs * p->entries, -1);
     p->length.assign(n_seqs, 0);
     p->free_bits.assign((size_t)n_blocks / 64 + 1, 0);
@@ -87,7 +102,7 @@ int mk_pages_resize(mk_pages* p, int n, const int32_t* seqs, const int32_t* leng
   // shared, and how many pages are free, depends on the sequences before it in
   // the list. The counts it lowers are written down and raised again.
   std::vector<uint8_t> seen;
-  std::vector<int32_t> lowered;
+  std::vector<int32_t> lowered, sources;
   const char* why = nullptr;
   int code = MK_ERR_INVALID, made = 0;
   try {
@@ -96,6 +111,7 @@ int mk_pages_resize(mk_pages* p, int n, const int32_t* seqs, const int32_t* leng
     for (int i = 0; i < n; ++i)
       if (seqs[i] >= 0 && seqs[i] < p->n_seqs) most += (size_t)p->used(p->length[seqs[i]]);
     lowered.reserve(most);
+    sources.reserve(std::min(n, p->n_seqs));
   } catch (const std::exception&) {
     return op_fail(MK_ERR_OOM, "no host memory");
   }
@@ -116,6 +132,8 @@ int mk_pages_resize(mk_pages* p, int n, const int32_t* seqs, const int32_t* leng
         ++made;
         --p->refs[t[u0 - 1]];
         lowered.push_back(t[u0 - 1]);
+        p->held[t[u0 - 1]] = 1;
+        sources.push_back(t[u0 - 1]);
       }
       if (free_now < 0) {
         why = "not enough free pages";
@@ -123,14 +141,17 @@ int mk_pages_resize(mk_pages* p, int n, const int32_t* seqs, const int32_t* leng
       }
     } else {
       for (int e = u1; e < u0; ++e) {
-        if (--p->refs[t[e]] == 0) ++free_now;
+        if (--p->refs[t[e]] == 0 && !p->held[t[e]]) ++free_now;
         lowered.push_back(t[e]);
       }
     }
   }
   for (int32_t b : lowered) ++p->refs[b];
   if (!why && made > capacity) why = "copies: capacity is too small";
-  if (why) return op_fail(code, why);
+  if (why) {
+    p->release(sources);
+    return op_fail(code, why);
+  }
 
   for (int i = 0; i < n; ++i) {
     int32_t* t = &p->table[(size_t)seqs[i] * p->entries];
@@ -151,6 +172,7 @@ int mk_pages_resize(mk_pages* p, int n, const int32_t* seqs, const int32_t* leng
     }
     p->length[seqs[i]] = lengths[i];
   }
+  p->release(sources);
   return MK_OK;
 }
 

@@ -488,7 +488,9 @@ int mk_cache_copy_blocks(const mk_cache* cache, const mk_block_copy* copies, int
    tables are what mk_decode_step_paged takes. Pages are shared by forked
    sequences; a sequence about to write into a partly filled page that others
    hold gets a copy of its own, which the caller makes with
-   mk_cache_copy_blocks before the write. The lowest free page is taken first.
+   mk_cache_copy_blocks before the write (one call for the copies of each
+   call here, in order). The lowest free page is taken first; a page that a copy
+   of the running call reads is not free before the next one.
    A failing call changes nothing. Not thread-safe per object. */
 typedef struct mk_pages mk_pages;
 int mk_pages_create(int n_blocks, int block_size, int n_seqs, int kv_capacity, mk_pages** out);

@@ -106,6 +106,27 @@ def test_lowest_page_first_and_copy_on_write():
     assert p.resize([], []).shape == (0, 3)
 
 
+def test_a_page_that_a_copy_reads_is_not_free_in_the_same_call():
+    p = mk.Pages(7, 4, 4, 16)
+    p.resize([0, 1], [6, 6])
+    p.fork([0, 1], [2, 3])
+    # 0 copies page 1, 2 then lets go of it, 1 needs a page for its own copy
+    assert p.resize([0, 2, 1], [7, 0, 7]).tolist() == [[1, 4, 2], [3, 5, 2]]
+    assert p.n_free() == 2 and p.resize([2], [8]).tolist() == []
+    assert p.table()[2, :2].tolist() == [1, 6]  # free again in the next call
+    p = mk.Pages(5, 4, 4, 16)  # the same without a page for it
+    p.resize([0, 1], [6, 6])
+    p.fork([0, 1], [2, 3])
+    before = state(p)
+    with pytest.raises(mk.MkError) as e:
+        p.resize([0, 2, 1], [7, 0, 7])
+    assert e.value.code == mk.MK_ERR_OOM
+    for a, b in zip(before, state(p)):
+        assert np.array_equal(a, b)
+    assert p.resize([0, 2], [7, 0]).tolist() == [[1, 4, 2]]
+    assert p.resize([1], [7]).tolist() == [[3, 1, 2]]
+
+
 def test_full_pages_are_shared_without_a_copy():
     p = mk.Pages(8, 4, 3, 16)
     p.resize(0, 8)
