@@ -49,29 +49,66 @@ int check_cache(const mk_cache* c, int batch, bool need_table, CacheView* out) n
 
 namespace {
 
-// ---- element access: eight consecutive elements of a row -----------------------
+// ---- element access: N = 1, 2, 4 or 8 consecutive elements, aligned to N elements ------
 
-struct Raw8 {
-  uint32_t w[8];  // bf16: four words; fp32: eight
-};
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, Raw8& r) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
-  if constexpr (sizeof(T) == 4) {
-    const uint4 b = *reinterpret_cast<const uint4*>(p + 4);
-    r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+// raw elements, in 32-bit words (bf16: two to a word; `at` is even unless N = 1)
+template <int N>
+__device__ __forceinline__ void load(const float* p, uint32_t* w, int at) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p + i);
+      w[at + i] = a.x, w[at + i + 1] = a.y, w[at + i + 2] = a.z, w[at + i + 3] = a.w;
+    }
+  } else if constexpr (N == 2) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    w[at] = a.x, w[at + 1] = a.y;
+  } else {
+    w[at] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load(const uint16_t* p, uint32_t* w, int at) {
+  if constexpr (N == 8) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[at / 2] = a.x, w[at / 2 + 1] = a.y, w[at / 2 + 2] = a.z, w[at / 2 + 3] = a.w;
+  } else if constexpr (N == 4) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    w[at / 2] = a.x, w[at / 2 + 1] = a.y;
+  } else if constexpr (N == 2) {
+    w[at / 2] = *reinterpret_cast<const uint32_t*>(p);
+  } else {
+    w[at / 2] = at & 1 ? w[at / 2] | (uint32_t)*p << 16 : *p;
   }
 }
 template <typename T>
-__device__ __forceinline__ float elem(const Raw8& r, int j) {
-  if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[j]);
-  else return (j & 1) ? bf_hi(r.w[j >> 1]) : bf_lo(r.w[j >> 1]);
+__device__ __forceinline__ float elem(const uint32_t* w, int j) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+  else return (j & 1) ? bf_hi(w[j >> 1]) : bf_lo(w[j >> 1]);
 }
-__device__ __forceinline__ uint4 pack_bf16(const float (&x)[8]) {
-  return make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]), bf16x2_rn(x[4], x[5]),
-                    bf16x2_rn(x[6], x[7]));
+template <int N>
+__device__ __forceinline__ void store(float* p, const float* x) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else {
+    *p = x[0];
+  }
+}
+template <int N>
+__device__ __forceinline__ void store(uint16_t* p, const float* x) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]),
+                                              bf16x2_rn(x[4], x[5]), bf16x2_rn(x[6], x[7]));
+  else if constexpr (N == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_rn(x[0], x[1]), bf16x2_rn(x[2], x[3]));
+  else if constexpr (N == 2)
+    *reinterpret_cast<uint32_t*>(p) = bf16x2_rn(x[0], x[1]);
+  else
+    *p = (uint16_t)bf16x2_rn(x[0], 0.f);
 }
 
 // ---- rotary positions and append ------------------------------------------------
@@ -90,18 +127,21 @@ struct RopeParams {
   int rows, T, nh, tokens;  // rows = batch * T; tokens per block
 };
 
-// How the rotated pairs lie in a head: neighbours; halves that are whole
-// 8-element chunks (the partner chunk sits in another lane of the head); any
-// other halves (the partner elements are loaded one by one).
-enum { kNeighbours, kHalves, kHalvesOdd };
-
 // A block takes `tokens` rows: one angle per (token, pair), shared by all heads
 // (sincospif of a fraction of a turn found by a 64-bit fixed-point product, so
-// that it is exact to 2^-64 turns at any position), then every head of q, k and
-// v, eight elements per lane, one head in D / 8 neighbouring lanes. All of a
-// head's loads come before its first store, so q_out may be q.
-// Bound by the bytes of the rows; four heads are in flight per lane (two: 4 % slower).
-template <typename T, int D, int PAIRS>
+// that it is exact to 2^-64 turns at any position). Then a warp takes heads of q,
+// k and v of one row, D / 8 lanes to a head. A lane has four pairs, both members
+// of each, so that its sines and cosines stay in its registers and nothing is
+// exchanged (q_out may be q). PIECE: elements that lie together for a lane, 8 when
+// the pairs are neighbours, else the largest of 4, 2, 1 that divides
+// rotary_dim / 2; the elements behind rotary_dim are taken as neighbours.
+// (Eight elements in a row per lane and the partners by shuffles: 218 us
+// against 132 for the 32768 rows below in halves of 64, 450 against 138 in
+// halves of 62, where the partners were loaded one by one.)
+// Bound by the bytes of the rows: 32768 rows of the 8B shape, bf16, 805 MB, take
+// 125 us as neighbours, 6.4 TB/s; U heads of a lane are in flight: 133 us with 2,
+// 136 with 8. 200 rows take 4 to 5 us, a launch's latency.
+template <typename T, int D, int PIECE>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
   __shared__ float2 cs[kRopeTokens][D / 2];
@@ -154,93 +194,74 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   }
   __syncthreads();
 
-  const int n_kv = p.cache.n_kv, heads = p.nh + 2 * n_kv, total = p.tokens * heads;
+  const int tok = warp % p.tokens;  // tokens divides WARPS
+  if (s_pos[tok] < 0) return;
+  const int n_kv = p.cache.n_kv, heads = p.nh + 2 * n_kv, step = WARPS / p.tokens * HPW;
   const int c = lane % LPH, half = p.rope.rotary_dim / 2;
-  for (int base = warp * HPW; base < total; base += U * WARPS * HPW) {
-    Raw8 x[U], y[U];
-    int tok[U], head[U];
+  const int64_t row = row0 + tok;
+  const uint32_t crow = s_row[tok];
+  // piece i of the lane (elements N i to N i + N - 1 of its eight) starts at `at`;
+  // elements j and j + 4 (neighbours: 2j and 2j + 1) are its pair j
+  constexpr int N = PIECE, FIRST = N == 8 ? 1 : 4 / N;
+  int at[8 / N];
+  if constexpr (N == 8) {
+    at[0] = 8 * c;
+  } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int item = base + u * WARPS * HPW + lane / LPH;
-      tok[u] = -1;
-      if (item < total) {
-        const int tk = item / heads;
-        head[u] = item - tk * heads;
-        if (s_pos[tk] >= 0) {
-          tok[u] = tk;
-          const int64_t row = row0 + tk;
-          const T* src;
-          if (head[u] < p.nh) src = (const T*)p.q + row * p.qs + head[u] * D;
-          else if (head[u] < p.nh + n_kv) src = (const T*)p.k + row * p.ks + (head[u] - p.nh) * D;
-          else src = (const T*)p.v + row * p.vs + (head[u] - p.nh - n_kv) * D;
-          load8(src + 8 * c, x[u]);
-          if constexpr (PAIRS == kHalvesOdd) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int e = 8 * c + j;
-              const int q = e < half ? e + half : e - half;
-              float f = 0.f;
-              if (e < 2 * half) {
-                if constexpr (sizeof(T) == 4) f = src[q];
-                else f = bf16f(src[q]);
-              }
-              y[u].w[j] = __float_as_uint(f);
-            }
-          }
-        }
-      }
+    for (int i = 0; i < FIRST; ++i) {
+      const int pair = 4 * c + N * i;
+      at[i] = pair < half ? pair : 2 * pair;
+      at[i + FIRST] = pair < half ? half + pair : 2 * pair + N;
     }
-    __syncwarp();
+  }
+  float2 w[4];
+  bool turns[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    turns[j] = 4 * c + j < half;
+    w[j] = cs[tok][4 * c + j];
+  }
+  for (int base = warp / p.tokens * HPW; base < heads; base += U * step) {
+    uint32_t x[U][2 * sizeof(T)];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if constexpr (PAIRS == kHalves) {
-        const int e = 8 * c;
-        const int from = lane + (e < half ? half / 8 : e < 2 * half ? -(half / 8) : 0);
+      const int head = base + u * step + lane / LPH;
+      if (head >= heads) continue;
+      const T* src;
+      if (head < p.nh) src = (const T*)p.q + row * p.qs + head * D;
+      else if (head < p.nh + n_kv) src = (const T*)p.k + row * p.ks + (head - p.nh) * D;
+      else src = (const T*)p.v + row * p.vs + (head - p.nh - n_kv) * D;
 #pragma unroll
-        for (int j = 0; j < (int)sizeof(T) * 2; ++j)
-          y[u].w[j] = __shfl_sync(0xffffffffu, x[u].w[j], from);
-      }
-      if (tok[u] < 0) continue;
-      const bool turned = head[u] < p.nh + n_kv;
+      for (int i = 0; i < 8 / N; ++i) load<N>(src + at[i], x[u], N * i);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int head = base + u * step + lane / LPH;
+      if (head >= heads) continue;
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = elem<T>(x[u], j);
-      if (turned) {
-        const float2* t = cs[tok[u]];
-        if constexpr (PAIRS == kNeighbours) {
+      if (head < p.nh + n_kv) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 w = t[4 * c + j];
-            const float a = o[2 * j], b = o[2 * j + 1];
-            o[2 * j] = a * w.x - b * w.y;
-            o[2 * j + 1] = a * w.y + b * w.x;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int e = 8 * c + j;
-            if (e < 2 * half) {
-              const float2 w = t[e < half ? e : e - half];
-              float f;
-              if constexpr (PAIRS == kHalves) f = elem<T>(y[u], j);
-              else f = __uint_as_float(y[u].w[j]);
-              o[j] = e < half ? o[j] * w.x - f * w.y : f * w.y + o[j] * w.x;
-            }
+        for (int j = 0; j < 4; ++j) {
+          const int i = N == 8 ? 2 * j : j, k = N == 8 ? 2 * j + 1 : j + 4;
+          const float a = o[i], b = o[k];
+          if (turns[j]) {
+            o[i] = a * w[j].x - b * w[j].y;
+            o[k] = a * w[j].y + b * w[j].x;
           }
         }
       }
-      if (head[u] < p.nh) {
-        T* dst = (T*)p.q_out + (int64_t)(row0 + tok[u]) * p.os + head[u] * D + 8 * c;
-        if constexpr (sizeof(T) == 4) {
-          *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<float4*>(dst + 4) = make_float4(o[4], o[5], o[6], o[7]);
-        } else {
-          *reinterpret_cast<uint4*>(dst) = pack_bf16(o);
-        }
-      } else if (s_row[tok[u]] != kNoRow) {
-        const int g = turned ? head[u] - p.nh : head[u] - p.nh - n_kv;
-        const size_t r = (size_t)s_row[tok[u]] + (size_t)g * p.cache.block_size;
-        *reinterpret_cast<uint4*>((turned ? p.k_cache : p.v_cache) + r * D + 8 * c) = pack_bf16(o);
+      auto put = [&](auto* dst) {
+#pragma unroll
+        for (int i = 0; i < 8 / N; ++i) store<N>(dst + at[i], o + N * i);
+      };
+      if (head < p.nh) {
+        put((T*)p.q_out + row * p.os + head * D);
+      } else if (crow != kNoRow) {
+        const bool key = head < p.nh + n_kv;
+        const int g = head - p.nh - (key ? 0 : n_kv);
+        put((key ? p.k_cache : p.v_cache) + ((size_t)crow + (size_t)g * p.cache.block_size) * D);
       }
     }
   }
@@ -250,9 +271,10 @@ template <typename T, int D>
 void launch_rope(const RopeParams& p, cudaStream_t st) {
   const dim3 grid((p.rows + p.tokens - 1) / p.tokens);
   const int half = p.rope.rotary_dim / 2;
-  if (p.rope.interleaved) rope_append_kernel<T, D, kNeighbours><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (half % 8 == 0) rope_append_kernel<T, D, kHalves><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_append_kernel<T, D, kHalvesOdd><<<grid, kRopeThreads, 0, st>>>(p);
+  if (p.rope.interleaved) rope_append_kernel<T, D, 8><<<grid, kRopeThreads, 0, st>>>(p);
+  else if (half % 4 == 0) rope_append_kernel<T, D, 4><<<grid, kRopeThreads, 0, st>>>(p);
+  else if (half % 2 == 0) rope_append_kernel<T, D, 2><<<grid, kRopeThreads, 0, st>>>(p);
+  else rope_append_kernel<T, D, 1><<<grid, kRopeThreads, 0, st>>>(p);
 }
 
 // ---- accepted rows moved down ------------------------------------------------------
@@ -489,7 +511,11 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
   p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.os = q_out_stride;
   p.starts = starts, p.parents = parents, p.counts = counts;
   p.rows = batch * n_tokens, p.T = n_tokens, p.nh = n_heads;
-  p.tokens = p.rows >= 4096 ? kRopeTokens : 1;
+  // Rows of a block: one where the blocks are few (8B shape, bf16, 512 rows: 6.2 us
+  // against 7.2 with four), four where there are enough, since a block's rows
+  // then find their angles together (1024 rows 7.2 us against 8.2 with one, 2048
+  // 11.0 against 14.1, 32768 126 against 168).
+  p.tokens = p.rows >= 1024 ? kRopeTokens : 1;
   cudaStream_t st = (cudaStream_t)stream;
   if (type == MK_TYPE_FP32) {
     if (cache->head_dim == 64) launch_rope<float, 64>(p, st);

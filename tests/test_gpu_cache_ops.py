@@ -2,6 +2,7 @@
 (tests/cache_ops_ref.py), at the sizes, masks and layouts where they can go
 wrong."""
 import itertools
+import math
 
 import numpy as np
 import pytest
@@ -409,6 +410,39 @@ def test_rope_far_positions(scaling):
         # the reference's own angle is off by 2^-53 x 2^20
         assert np.abs(got[0, t] - want).max() <= host(q).__abs__().max() * 2 * m * 4 * 2**-22
     assert (pool[0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("D,part", [(64, 62), (64, 60), (64, 40), (128, 10), (128, 100), (128, 128)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T", [70, 1027])
+def test_rope_layouts(T, interleaved, D, part, dtype):
+    """Halves of every alignment, short and long calls; what lies behind
+    rotary_dim comes through bit by bit, infinities and NaN too, and stays out
+    of the pairs."""
+    nh, nkv, start = 3, 2, 5
+    kc = torch.zeros((1, nkv, T + start, D), dtype=BF16, device=dev())
+    vc = torch.zeros_like(kc)
+    q = torch.randn((1, T, nh, D), device=dev()).to(dtype)
+    kn = torch.randn((1, T, nkv, D), device=dev()).to(dtype)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0], device=dev())
+    for x in (q, kn):
+        x[:, ::3, :, part:] = odd.repeat(D)[:D - part].to(dtype)
+    qh, kh = host(q), host(kn)
+    out = mk.rope_append(mk.Rope(D, rotary_dim=part, interleaved=interleaved),
+                         mk.Cache([kc], [vc]), 0, q, kn, kn, ints([start]), q_out=q)
+    f, m = ref.frequencies(part, 10000.0)
+    got, keys = host(out)[0], host(kc)[0]
+    rest = dict(equal_nan=True)
+    assert np.array_equal(got[..., part:], qh[0, ..., part:], **rest)
+    assert np.array_equal(keys[:, start:, part:], host(kn.to(BF16))[0, ..., part:].swapaxes(0, 1), **rest)
+    assert np.array_equal(host(vc)[0, :, start:], host(kn.to(BF16))[0].swapaxes(0, 1), **rest)
+    for t in {0, 1, 33, T - 3, T - 2, T - 1}:
+        for x, y, r in ((qh[0, t], got[t], 2**-8 if dtype == BF16 else 2**-24),
+                        (kh[0, t], keys[:, start + t], 2**-8)):
+            want = ref.rotate(x[:, :part], start + t, f, m, interleaved)
+            near = np.abs(x[:, :part]).max() * 4 * 2**-22 + r * np.abs(want)
+            assert (np.abs(y[:, :part] - want) <= near).all()
 
 
 def test_rope_prompt_in_place_and_bounds():
