@@ -703,6 +703,8 @@ def cache_compact(cache: Cache, starts, path, accepted, stream=None):
 
 def _host_ints(x) -> np.ndarray:
     """A contiguous host int32 array of x (whole numbers only)."""
+    if type(x) is np.ndarray and x.dtype == np.int32 and x.flags.c_contiguous:
+        return x
     a = np.asarray(x)
     if a.dtype != np.int32:
         if a.size and (a.dtype.kind not in "iu" or a.min() < -2**31 or a.max() >= 2**31):
@@ -743,23 +745,23 @@ class Pages:
 
     @staticmethod
     def _pair(a, b, what: str):
-        a, b = _host_ints(a).reshape(-1), _host_ints(b).reshape(-1)
-        if a.shape != b.shape:
+        a, b = _host_ints(a), _host_ints(b)
+        if a.size != b.size:
             raise _bad(f"{what} must be two lists of the same length")
         return a, b
 
     def resize(self, seqs, lengths) -> np.ndarray:
         """mk_pages_resize (0: gives a sequence's pages back)."""
         s, n = self._pair(seqs, lengths, "seqs, lengths")
-        copies, made = np.empty((len(s), 3), np.int32), ctypes.c_int()
-        _check(lib().mk_pages_resize(self.h, len(s), _at(s), _at(n), _at(copies), len(s),
+        copies, made = np.empty((s.size, 3), np.int32), ctypes.c_int()
+        _check(lib().mk_pages_resize(self.h, s.size, _at(s), _at(n), _at(copies), s.size,
                                      ctypes.byref(made)))
         return copies[:made.value]
 
     def fork(self, parents, children):
         """mk_pages_fork: each empty child becomes a fork of its parent."""
         p, c = self._pair(parents, children, "parents, children")
-        _check(lib().mk_pages_fork(self.h, len(p), _at(p), _at(c)))
+        _check(lib().mk_pages_fork(self.h, p.size, _at(p), _at(c)))
 
     def compact(self) -> np.ndarray:
         """mk_pages_compact: the pages in use renumbered to the lowest ones."""

@@ -34,7 +34,12 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 // bf16 (relative 2^-8, the size of the output's own rounding); sums, maxima and
 // the output accumulate in fp32. A tile is 16 KB of keys and 16 KB of values
 // whatever the head's size: 64-key tiles of 64 dimensions spent their time on the
-// barriers between them.
+// barriers between them. Three tiles per block and two blocks per SM keep 192 KB
+// per SM in flight. Bound by the bytes of the keys and values: a single bf16 token of
+// 8 sequences over 16384 keys each (8B shape, 537 MB) takes 88 us, 6.1 TB/s; fp32
+// 134 us, bound by its six products and the splitting. Short contexts are bound by
+// latency: 512 keys of one sequence 9.1 us, two launches of which the second
+// waits for the first inside.
 constexpr int tile_keys(int D) { return 8192 / D; }
 
 template <int D, int P>
@@ -434,7 +439,9 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
 // fixed order. Many: a warp takes a row (four one after another took 6 us longer
 // on 6400 rows). A lane has D / 32 of the row's columns; the lanes read the
 // shares' maxima and sums 32 at a time, so that every share's factor is known
-// before its columns are read.
+// before its columns are read. Bound by latency: it starts while the other kernel
+// runs, has its line of work by the time that ends, and then reads twice in a row
+// (the factors, the columns), about 4 us.
 template <int D, bool FEW, typename T>
 __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant__ AttnParams p) {
   constexpr int E = D / 32, TURNS = FEW ? 4 : 1, U = FEW ? 8 : 2;  // U: loads in flight
@@ -550,6 +557,18 @@ struct Plan {
 // products are that size; more to the tensor-memory kernel: bf16 activations in
 // two streams of up to 128 rows each (up to 128 rows: two streams over the same
 // rows that take turns at the key tiles), fp32 ones in tiles of 128 rows.
+// Warp-level against tensor-memory kernel, us:
+//   8 sequences over 16384 keys, 8B shape, bf16   4 nodes (16 rows)  93.2    93.5
+//                                                 5 nodes (20 rows) 147.6    94.2
+//                                          fp32   4 nodes           139.9   130.3
+//                                                 5 nodes           252.0   130.9
+//   one sequence over 1024 keys, 8B shape, bf16   1 node             11.3    13.3
+//                                                 5 nodes            14.3    14.0
+//   4 sequences over 4096 keys, 1B shape, fp32    4 nodes            18.5    22.6
+// Two blocks of up to 128 rows in a pass over the keys against a pass for each (bf16,
+// 8 sequences over 16384 keys): 132 rows 112 us against 132, 256 rows 128 against
+// 141; the lengths are not known here, and one sequence over 2048 keys, where the
+// second block's share only adds to the first's, takes 31 us against 27.
 Plan plan_of(int T, int G, int D, int type, int n_sm) {
   Plan pl;
   const int rows = T * G;

