@@ -345,6 +345,14 @@ def test_attention_many_sequences():
     check_attention(rng, B, 2, 4, 2, 64, BF16, 8, starts, counts=rng.integers(0, 3, B))
 
 
+@pytest.mark.parametrize("T,nh,nkv,dtype", [(1, 2, 1, BF16), (9, 2, 1, BF16), (17, 2, 2, FP32)])
+def test_attention_as_many_sequences_as_there_may_be(T, nh, nkv, dtype):
+    """1024 sequences, of which some have no node, on both kernels."""
+    rng = np.random.default_rng(T)
+    check_attention(rng, 1024, T, nh, nkv, 64, dtype, 16, rng.integers(0, 40, 1024),
+                    counts=rng.integers(0, T + 1, 1024))
+
+
 # ---- rotary positions and append -------------------------------------------------------
 
 
@@ -526,6 +534,21 @@ def test_accept(B, T, V, dtype):
     assert T < 30 or want[2].max() > 2
     check_accept(logits, tokens, None, counts)
     check_accept(logits, tokens, make_parents(rng, B, T, "odd"), counts)
+
+
+@pytest.mark.parametrize("B,T,V,taken", [(3, 300, 77, [300, 1, 129]), (1024, 63, 5, None)])
+def test_accept_long_chains_and_many_sequences(B, T, V, taken):
+    rng = np.random.default_rng(T)
+    tokens = rng.integers(0, V, (B, T))
+    logits = torch.randn((B, T, V), device=dev())
+    taken = rng.integers(1, T + 1, B) if taken is None else taken
+    for b, n in enumerate(taken):
+        logits[b, torch.arange(n - 1), torch.as_tensor(tokens[b, 1:n])] = 9.0
+        if n < T:
+            logits[b, n - 1, (tokens[b, n] + 1) % V] = 9.0
+    want = check_accept(logits, tokens, None, None)
+    assert list(want[2]) == list(taken)
+    check_accept(logits, tokens, None, [T // 2] * B)
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
