@@ -36,8 +36,9 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 // whatever the head's size: 64-key tiles of 64 dimensions spent their time on the
 // barriers between them. Three tiles per block and two blocks per SM keep 192 KB
 // per SM in flight. Bound by the bytes of the keys and values: a single bf16 token of
-// 8 sequences over 16384 keys each (8B shape, 537 MB) takes 88 us, 6.1 TB/s; fp32
-// 134 us, bound by its six products and the splitting. Short contexts are bound by
+// 8 sequences over 16384 keys each (8B shape, 537 MB) takes 88 us, 6.1 TB/s; fp32 in
+// heads of 64 (1B shape, 268 MB) 71 us, bound by its six products and the
+// splitting. Short contexts are bound by
 // latency: 512 keys of one sequence 9.1 us, two launches of which the second
 // waits for the first inside.
 constexpr int tile_keys(int D) { return 8192 / D; }
@@ -554,17 +555,24 @@ struct Plan {
 };
 
 // Which kernel, and its tiles. Up to 16 rows go to the warp-level kernel, whose
-// products are that size; more to the tensor-memory kernel: bf16 activations in
-// two streams of up to 128 rows each (up to 128 rows: two streams over the same
-// rows that take turns at the key tiles), fp32 ones in tiles of 128 rows.
+// products are that size, but for fp32 with heads of 128, whose six products are
+// too much for it; the others to the tensor-memory kernel: bf16 activations in two
+// streams of up to 128 rows each (up to 128 rows: two streams over the same rows
+// that take turns at the key tiles), fp32 ones in tiles of 128 rows, or, up to 32
+// rows, with the parts of the weights stacked.
 // Warp-level against tensor-memory kernel, us:
 //   8 sequences over 16384 keys, 8B shape, bf16   4 nodes (16 rows)  93.2    93.5
 //                                                 5 nodes (20 rows) 147.6    94.2
-//                                          fp32   4 nodes           139.9   130.3
-//                                                 5 nodes           252.0   130.9
+//                                          fp32   1 node            133.7   103.9
+//                                                 4 nodes           140.0   107.0
+//                                1B shape, fp32   4 nodes            72.1    82.0
+//   8 sequences over 1024 keys,  8B shape, fp32   1 node             21.8    24.4
+//                                                 4 nodes            26.7    27.7
 //   one sequence over 1024 keys, 8B shape, bf16   1 node             11.3    13.3
 //                                                 5 nodes            14.3    14.0
-//   4 sequences over 4096 keys, 1B shape, fp32    4 nodes            18.5    22.6
+//   4 sequences over 4096 keys,  1B shape, fp32   4 nodes            18.5    22.6
+// fp32 parts stacked against one after another (8 sequences over 16384 keys, 8 nodes): 8B
+// shape 111 us against 129, 1B shape 83 against 94.
 // Two blocks of up to 128 rows in a pass over the keys against a pass for each (bf16,
 // 8 sequences over 16384 keys): 132 rows 112 us against 132, 256 rows 128 against
 // 141; the lengths are not known here, and one sequence over 2048 keys, where the
@@ -572,13 +580,13 @@ struct Plan {
 Plan plan_of(int T, int G, int D, int type, int n_sm) {
   Plan pl;
   const int rows = T * G;
-  pl.tc = rows > kRows;
+  pl.tc = rows > kRows || (type == MK_TYPE_FP32 && D == 128);
   // measured at 0 to 8: 25 nodes over 128 to 4096 keys (1B shape, 8 sequences) 32.8 us
   // at 0, 25.2 at 2, 23.1 at 4, 24.2 at 8; the other cases within 2 % from 2 to 8
   pl.extra = 4;
   if (pl.tc && type == MK_TYPE_FP32) {
     pl.tile = 128;
-    pl.row_tile = 128;
+    pl.row_tile = rows <= 32 ? 32 : 128;
     pl.row_tiles = (rows + 127) / 128;
     pl.groups = std::max(1, n_sm / pl.row_tiles);
   } else if (pl.tc) {
@@ -639,7 +647,7 @@ template <int D>
 int launch_all(const AttnParams& p, const Plan& pl, int type, cudaStream_t st) {
   int rc;
   if (pl.tc) rc = launch_tree_attention_tc(p, D, type, st);
-  else if (type == MK_TYPE_FP32) rc = launch<D, 3>(p, st);
+  else if (D == 64 && type == MK_TYPE_FP32) rc = launch<64, 3>(p, st);
   else rc = launch<D, 1>(p, st);
   if (rc) return rc;
   cudaLaunchAttribute attr;

@@ -18,7 +18,9 @@
 // weights' rounding to bf16 (relative 2^-8) is the size of the output's own.
 //
 // fp32 activations. Queries and weights go in as three bf16 parts (2^-24 of the
-// value), each product runs once per part. The matrix unit truncates as it
+// value), each product runs once per part; up to 32 rows stand three times in the
+// block, each time with another part of the weights, so that the weights' products
+// run once. The matrix unit truncates as it
 // accumulates, which over a long context costs more than fp32's own rounding, so
 // it sums one tile only (two score buffers, one product) and the rows' threads
 // add the tiles up in registers. (Accumulated in tensor memory the error against
@@ -35,10 +37,12 @@
 // us, 5.6 TB/s, bound by the bytes; with 256 rows 128 us, 4.3 TB/s and 1.08 PFLOP/s,
 // bound by the chain from a tile's scores through their softmax and weights to the
 // next scores (3150 cycles a tile, 2000 of them softmax, two tiles in flight);
-// fp32 with 24 rows 131 us, with 256 rows 269 us (in bf16 parts 1.5 PFLOP/s).
+// fp32 with 32 rows 111 us, with 256 rows 259 us (in bf16 parts 1.6 PFLOP/s).
 //
 // Every wait ends: after kWaitNs a thread stops waiting for good and goes on, and
 // the rows of the block come out as NaN.
+#include <type_traits>
+
 #include "mk_tree_attention.cuh"
 
 namespace mk {
@@ -178,18 +182,22 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Kinds of call: bf16 with one or two row blocks, fp32.
-enum { kOne, kTwo, kExact };
+// Kinds of call: bf16 with one or two row blocks, fp32 with up to 128 or 32 rows.
+enum { kOne, kTwo, kExact, kFew };
 
 constexpr int kKeys = 128;  // keys of a tile
 
 // Columns of tensor memory (512): kOne, kTwo: scores (weights over them) of stream
 // s at 128 s, its output at 256 + D s. kExact: scores of tile parity s, the three
-// parts of the weights over them, at 192 s, a tile's product at 384.
+// parts of the weights over them, at 192 s, a tile's product at 384. kFew: scores
+// (weights over them) of tile parity s at 128 s, the tile's product at 256 + D s.
 template <int D, int KIND>
 struct Layout {
   static constexpr bool TWO = KIND == kTwo;
-  static constexpr int PARTS = KIND == kExact ? 3 : 1;
+  static constexpr bool EXACT = KIND == kExact || KIND == kFew;
+  static constexpr int PARTS = EXACT ? 3 : 1;             // of the queries
+  static constexpr int WEIGHT_PARTS = KIND == kExact ? 3 : 1;  // one after another
+  static constexpr int PRODUCTS = KIND == kExact ? 1 : 2;      // outputs or products
   static constexpr int kScoreStep = KIND == kExact ? 192 : 128;
   static constexpr int kOut = 2 * kScoreStep;
   static constexpr int kBuf = kKeys * D * 2;  // a K or V tile
@@ -212,9 +220,9 @@ struct Shared {
   uint32_t odd[2];
   uint32_t odd_at[2][MK_MAX_TREE][2][4];
   float ml[128][2];                // kOne: stream 1's (m, l)
-  // kExact: a tile's product is in tensor memory / has been read; the halves'
+  // fp32: a tile's product is in tensor memory / has been read; the halves'
   // maxima (by tile parity) and sums
-  uint64_t t_full, t_free;
+  uint64_t t_full[2], t_free[2];
   float top[2][2][128], sum[2][128];
 };
 
@@ -371,7 +379,7 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
   Waiter wait(sm);
   uint32_t buf = 0, round = 0;
   uint32_t p_uses[2] = {0, 0};
-  uint32_t t_uses = 0;
+  uint32_t t_uses[2] = {0, 0};
   int u = u_begin;
   Share sh;
   // S of stream s from the K tile in buffer `at`; free: it is not needed again
@@ -393,28 +401,31 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
     }
     __syncwarp();
   };
-  // Weights of stream (kExact: tile parity) s times the V tile in buffer `at`: into
-  // the stream's output (add: to what is there), kExact: into the tile's product
+  // Weights of stream (fp32: tile parity) s times the V tile in buffer `at`: into
+  // the stream's output (add: to what is there), fp32: into the tile's product
   auto values = [&](int s, uint32_t at, bool add, bool free) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       wait(&sm.p_full[s][h], p_uses[s]);
-      if (KIND == kExact && h == 0) wait(&sm.t_free, t_uses++ + 1);
+      if (Lay::EXACT && h == 0) {
+        wait(&sm.t_free[s % Lay::PRODUCTS], t_uses[s % Lay::PRODUCTS] + 1);
+        ++t_uses[s % Lay::PRODUCTS];
+      }
       tc_fence_after();
       if (elect_one()) {
         const uint64_t v = operand(ring + at * Lay::kBuf, kKeys * 128);
 #pragma unroll
-        for (int part = Lay::PARTS - 1; part >= 0; --part)
+        for (int part = Lay::WEIGHT_PARTS - 1; part >= 0; --part)
 #pragma unroll
           for (int i = 4 * h; i < 4 * h + 4; ++i)
-            mma_tmem(tmem + Lay::kOut + (KIND == kExact ? 0 : s * D),
+            mma_tmem(tmem + Lay::kOut + s % Lay::PRODUCTS * D,
                      tmem + s * Lay::kScoreStep + part * 64 + i * 8, v + i * (2048 / 16), kValues,
-                     h > 0 || part < Lay::PARTS - 1 || i > 0 ? 1u : add);
+                     h > 0 || part < Lay::WEIGHT_PARTS - 1 || i > 0 ? 1u : add);
         if (h == 1) {
           if (free) tc_commit(&sm.empty[at]);
-          if (KIND == kExact) {
-            tc_commit(&sm.t_full);
-            mbar_arrive(&sm.t_full);  // hands on the tile's odd values
+          if (Lay::EXACT) {
+            tc_commit(&sm.t_full[s % Lay::PRODUCTS]);
+            mbar_arrive(&sm.t_full[s % Lay::PRODUCTS]);  // hands on the tile's odd values
           }
         }
       }
@@ -455,11 +466,11 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
       for (int s = 0; s < 2 && s < sh.n; ++s) scores(s, take(), true);
       for (int j = 0; j < sh.n; ++j) {
         const int s = j & 1;
-        values(s, take(), KIND != kExact && j >= 2, true);
+        values(s, take(), !Lay::EXACT && j >= 2, true);
         if (j + 2 < sh.n) scores(s, take(), true);
       }
     }
-    if (KIND != kExact && elect_one()) {
+    if (!Lay::EXACT && elect_one()) {
       tc_commit(&sm.o_full);
       mbar_arrive(&sm.o_full);
     }
@@ -615,19 +626,19 @@ __device__ __forceinline__ float2 weights2(uint32_t a, uint32_t b, unsigned long
   return w;
 }
 
-// Two weights (finite, not negative) as three bf16 parts each: the upper 8 bits of
-// the significand, the next 8, the last 8, so the parts' sum is the weight.
-__device__ __forceinline__ void split_exactly(float2 w, uint32_t& a, uint32_t& b, uint32_t& c) {
-  const uint32_t x = __float_as_uint(w.x), y = __float_as_uint(w.y);
-  a = __byte_perm(x, y, 0x7632);  // the upper halves
-  unsigned long long rest = pack2(w.x, w.y);
-  add2(rest, pack2(-__uint_as_float(x & 0xffff0000u), -__uint_as_float(y & 0xffff0000u)));
-  const float2 r = unpack2(rest);
-  const uint32_t rx = __float_as_uint(r.x), ry = __float_as_uint(r.y);
-  b = __byte_perm(rx, ry, 0x7632);
-  add2(rest, pack2(-__uint_as_float(rx & 0xffff0000u), -__uint_as_float(ry & 0xffff0000u)));
-  const float2 q = unpack2(rest);
-  c = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632);
+// Part q of two weights (finite, not negative), as bf16: the upper 8 bits of the
+// significand, the next 8, the last 8, so that the three parts' sum is the weight.
+template <int q>
+__device__ __forceinline__ uint32_t weight_part(float2 w) {
+  constexpr uint32_t kUpTo = q == 0 ? ~0u : q == 1 ? 0xffffff00u : ~0u, kFrom = q == 1 ? 0xffff0000u : 0xffffff00u;
+  uint32_t x = __float_as_uint(w.x), y = __float_as_uint(w.y);
+  if (q > 0) {
+    unsigned long long part = pack2(__uint_as_float(x & kUpTo), __uint_as_float(y & kUpTo));
+    add2(part, pack2(-__uint_as_float(x & kFrom), -__uint_as_float(y & kFrom)));
+    const float2 z = unpack2(part);
+    x = __float_as_uint(z.x), y = __float_as_uint(z.y);
+  }
+  return __byte_perm(x, y, 0x7632);  // the upper halves
 }
 
 // 32 columns of a finished row: the odd values it sees added, then written out
@@ -826,27 +837,32 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
   }
 }
 
-// kExact: a row has two threads, half 0 in warps 0-3 and half 1 in warps 4-7. Each
+// fp32: a row has two threads, half 0 in warps 0-3 and half 1 in warps 4-7. Each
 // makes the weights of half of every tile's keys (their maxima meet in shared
 // memory) and keeps half of the row's output columns in registers, to which it
 // adds a tile's product while the next one is made.
-template <int D>
+// kFew: the rows stand three times in the block, rows 32 i to 32 i + 31 with part i of
+// the weights, so that one product takes all three parts; the three sums are
+// added at the end of the share.
+template <int D, int KIND>
 __device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, const Line& line,
                                            uint8_t* q_ptr, uint32_t tmem, int u_begin, int u_end,
                                            int rt, int group) {
-  using Lay = Layout<D, kExact>;
+  using Lay = Layout<D, KIND>;
+  constexpr bool FEW = KIND == kFew;
   const int half = threadIdx.x / 128, r = threadIdx.x % 128, lane = threadIdx.x % 32;
+  const int copy = FEW ? r / 32 : 0;
   const uint32_t lanes = (uint32_t)(r / 32) * 32 << 16;
   const uint32_t t_o = tmem + lanes + Lay::kOut + half * (D / 2);
   const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2);
   Waiter wait(sm);
-  uint32_t s_uses[2] = {0, 0}, tile_no = 0;
+  uint32_t s_uses[2] = {0, 0}, t_uses[2] = {0, 0}, tile_no = 0;
   int u = u_begin;
   Share sh;
   for (uint32_t share = 0; next_share(p, line, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
-    const int row = rt * p.row_tile + r;
-    const bool live = row < sh.rows, warp_live = __any_sync(0xffffffffu, live);
+    const int row = rt * p.row_tile + (FEW ? lane : r);
+    const bool live = row < sh.rows && copy < 3, warp_live = __any_sync(0xffffffffu, live);
     load_query<D, 3>(p, sh, row, live, r, q_ptr, half * (D / 16), (half + 1) * (D / 16));
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full);
@@ -880,17 +896,31 @@ __device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, cons
           const unsigned long long from2 = pack2(from, from);
           unsigned long long sums[2] = {0, 0};
           __syncwarp();
+          // the weights, and their parts FIRST to LAST put down
+          auto put_weights = [&](auto first_part, auto last_part) {
+            constexpr int FIRST = decltype(first_part)::value, LAST = decltype(last_part)::value;
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            uint32_t w[3][8];
+            for (int h = 0; h < 4; ++h) {
+              uint32_t w[3][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 a = weights2(x[16 * h + 2 * e], x[16 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
-              split_exactly(a, w[0][e], w[1][e], w[2][e]);
+              for (int e = 0; e < 8; ++e) {
+                const float2 a = weights2(x[16 * h + 2 * e], x[16 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
+                w[0][e] = weight_part<0>(a);
+                w[1][e] = weight_part<1>(a);
+                w[2][e] = weight_part<2>(a);
+              }
+#pragma unroll
+              for (int q = FIRST; q <= LAST; ++q)
+                tmem_store8(t_s + (q - FIRST) * 64 + 32 * half + 8 * h, w[q]);
             }
-#pragma unroll
-            for (int q = 0; q < 3; ++q) tmem_store8(t_s + q * 64 + 32 * half + 8 * h, w[q]);
-          }
+          };
+          using Part0 = std::integral_constant<int, 0>;
+          using Part1 = std::integral_constant<int, 1>;
+          using Part2 = std::integral_constant<int, 2>;
+          if (!FEW) put_weights(Part0{}, Part2{});
+          else if (copy == 0) put_weights(Part0{}, Part0{});
+          else if (copy == 1) put_weights(Part1{}, Part1{});
+          else put_weights(Part2{}, Part2{});
           add2(sums[0], sums[1]);
           const float2 sum = unpack2(sums[0]);
           l += sum.x + sum.y;
@@ -901,30 +931,42 @@ __device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, cons
         if (lane == 0) mbar_arrive(&sm.p_full[s][half]);
       }
       if (j > 0) {
-        wait(&sm.t_full, tile_no + j - 1);
+        const int t = FEW ? (j - 1) & 1 : 0;
+        wait(&sm.t_full[t], t ? t_uses[1]++ : t_uses[0]++);
         tc_fence_after();
         if (warp_live) {
 #pragma unroll
           for (int c = 0; c < D / 2; c += 32) {
-            uint32_t t[32];
-            tmem_load32(t_o + c, t);
+            uint32_t y[32];
+            tmem_load32(t_o + t * D + c, y);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[c + e] = fmaf(acc[c + e], last_keep, __uint_as_float(t[e]));
+            for (int e = 0; e < 32; ++e) acc[c + e] = fmaf(acc[c + e], last_keep, __uint_as_float(y[e]));
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.t_free);
+        if (lane == 0) mbar_arrive(&sm.t_free[t]);
       }
     }
     tile_no += sh.n;
     sm.sum[half][r] = l;
+    // The share's products are done, so the queries' place is free for the sums
+    // of the second and third parts.
+    float* other = reinterpret_cast<float*>(q_ptr) + half * (D / 2) * 32 + lane;
+    if (FEW && warp_live && copy > 0) {
+#pragma unroll
+      for (int e = 0; e < D / 2; ++e) other[((copy - 1) * D + e) * 32] = acc[e];
+    }
     named_bar(1, 32 * kSoftWarps);
-    if (warp_live) {
+    if (warp_live && copy == 0) {
+      if (FEW) {
+#pragma unroll
+        for (int e = 0; e < D / 2; ++e) acc[e] += other[(D + e) * 32] + other[e * 32];
+      }
       l = sm.sum[0][r] + sm.sum[1][r];
       if (wait_failed(sm)) l = NAN;
-      const size_t slot = part_slot(p, group, sh.begins, rt) * p.row_tile + r;
+      const size_t slot = part_slot(p, group, sh.begins, rt) * p.row_tile + (FEW ? lane : r);
 #pragma unroll
       for (int c = 0; c < D / 2; c += 32) {
         float y[32];
@@ -965,13 +1007,13 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
       mbar_init(&sm.s_full[s], 2);
       mbar_init(&sm.p_full[s][0], 4);
       mbar_init(&sm.p_full[s][1], 4);
+      mbar_init(&sm.t_full[s], 2);
+      mbar_init(&sm.t_free[s], kSoftWarps);
       mbar_init(&sm.done[s], kSoftWarps);
       sm.odd[s] = 0;
     }
     mbar_init(&sm.q_full, kSoftWarps);
     mbar_init(&sm.o_full, 2);
-    mbar_init(&sm.t_full, 2);
-    mbar_init(&sm.t_free, kSoftWarps);
     sm.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -990,8 +1032,8 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   // copy, because each waited for the last one's operands to be read).
   if (warp < kSoftWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    if constexpr (KIND == kExact) {
-      exact_role<D>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
+    if constexpr (Lay::EXACT) {
+      exact_role<D, KIND>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
     } else {
       softmax_role<D, KIND>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
     }
@@ -1022,12 +1064,12 @@ int launch(const AttnParams& p, cudaStream_t st) {
 }  // namespace
 
 int launch_tree_attention_tc(const AttnParams& p, int head_dim, int type, cudaStream_t st) {
-  const bool two = p.row_tile > 128;
+  const bool two = p.row_tile > 128, few = p.row_tile == 32;
   if (head_dim == 64)
-    return type == MK_TYPE_FP32 ? launch<64, kExact>(p, st)
+    return type == MK_TYPE_FP32 ? (few ? launch<64, kFew>(p, st) : launch<64, kExact>(p, st))
            : two                ? launch<64, kTwo>(p, st)
                                 : launch<64, kOne>(p, st);
-  return type == MK_TYPE_FP32 ? launch<128, kExact>(p, st)
+  return type == MK_TYPE_FP32 ? (few ? launch<128, kFew>(p, st) : launch<128, kExact>(p, st))
          : two                ? launch<128, kTwo>(p, st)
                               : launch<128, kOne>(p, st);
 }
