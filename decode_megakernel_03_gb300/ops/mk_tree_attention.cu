@@ -77,7 +77,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   griddep_launch();
   if (warp == 0) work_line(p, line);
   __syncthreads();
-  const Cut cut(line.prefix[p.B], p.groups);
+  const Cut cut(line.prefix[p.B], p);
   const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
   int u = u_begin;
 
@@ -454,11 +454,11 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
   if (warp == 0) work_line(p, line);
   __syncthreads();
   const int row = FEW ? blockIdx.x : blockIdx.x * 4 + warp;
-  const int places = (line.prefix[b + 1] - line.prefix[b]) / p.cache.n_kv;
+  const int places = line.prefix[b + 1] == line.prefix[b] ? 0 : places_of(p, min(line.start[b] + line.count[b], p.cache.capacity));
   const int rt = row / p.row_tile, r = row - rt * p.row_tile;
   bool cut_up = places > 0 && row < line.count[b] * p.G;
   int g0 = 0, g1 = 0, item0 = 0;
-  const Cut cut(line.prefix[p.B], p.groups);
+  const Cut cut(line.prefix[p.B], p);
   if (cut_up) {
     item0 = line.prefix[b] + g * places;
     g0 = cut.group_of(item0 + p.extra);
@@ -716,7 +716,9 @@ int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens,
   p.q = q, p.out = out, p.qs = q_stride, p.os = out_stride;
   p.starts = starts, p.parents = parents, p.counts = counts;
   p.B = batch, p.T = n_tokens, p.nh = n_heads, p.G = n_heads / cache->n_kv_heads;
-  p.tile = pl.tile, p.extra = pl.extra, p.row_tile = pl.row_tile, p.row_tiles = pl.row_tiles, p.groups = pl.groups;
+  p.tile_log2 = pl.tile == 128 ? 7 : 6;
+  p.extra = pl.extra, p.row_tile = pl.row_tile, p.row_tiles = pl.row_tiles, p.groups = pl.groups;
+  p.inv_groups = (uint32_t)std::min<uint64_t>((1ull << 32) / pl.groups + 1, UINT32_MAX);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + pl.o_floats;

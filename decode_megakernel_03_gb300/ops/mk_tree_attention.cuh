@@ -30,10 +30,11 @@ struct AttnParams {
   int64_t qs, os;
   const int32_t *starts, *parents, *counts;
   int B, T, nh, G;
-  int tile;                    // keys of a tile
+  int tile_log2;               // keys of a tile
   int extra;                   // tiles that a share's beginning and end are worth
   int row_tile;                // rows of a row tile
   int row_tiles, groups;       // grid = groups x row_tiles, row tiles fastest
+  uint32_t inv_groups;         // floor(2^32 / groups) + 1, at most 2^32 - 1
   float scale_log2;            // scale * log2(e)
   float* part_o;               // [groups][2][row_tiles][row_tile][D]
   float* part_ml;              // [groups][2][row_tiles][row_tile][2]: (max, sum)
@@ -41,8 +42,9 @@ struct AttnParams {
 
 // ---- the line of work -----------------------------------------------------------
 // Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), each is
-// `extra` places and then its tiles in order.
-
+// `extra` places and then its tiles in order. A block finds its part of the line
+// before it can fetch anything, so that this part has one division left (five took
+// 1000 of the 5000 cycles before the first copy).
 
 // The line in shared memory: the places of the sequences before b, and the
 // sequences' starts and counts (at their bounds).
@@ -51,6 +53,11 @@ struct Line {
   int start[kMaxSeqs];
   uint8_t count[kMaxSeqs];
 };
+
+// places of an item with `keys` keys
+__device__ __forceinline__ int places_of(const AttnParams& p, int keys) {
+  return ((keys + (1 << p.tile_log2) - 1) >> p.tile_log2) + p.extra;
+}
 
 // Fills it with one warp. (The host makes sure that the line has fewer than 2^31
 // places.)
@@ -65,7 +72,7 @@ __device__ __forceinline__ void work_line(const AttnParams& p, Line& line) {
       line.start[b] = start;
       line.count[b] = (uint8_t)count;
       const int keys = count > 0 ? min(start + count, p.cache.capacity) : 0;
-      if (keys > 0) x = ((keys + p.tile - 1) / p.tile + p.extra) * p.cache.n_kv;
+      if (keys > 0) x = places_of(p, keys) * p.cache.n_kv;
     }
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -83,17 +90,23 @@ __device__ __forceinline__ void work_line(const AttnParams& p, Line& line) {
 // begin(s) = floor(s W / groups) = s q + floor(s r / groups).
 struct Cut {
   int W, groups, q, r;
-  __device__ __forceinline__ Cut(int W_, int groups_) : W(W_), groups(groups_) {
-    q = W / groups;
+  uint32_t inv;
+  __device__ __forceinline__ Cut(int W_, const AttnParams& p)
+      : W(W_), groups(p.groups), inv(p.inv_groups) {
+    q = (int)__umulhi((uint32_t)W, inv);  // at most one off, as W < 2^31
     r = W - q * groups;
+    if (r < 0) --q, r += groups;
+    if (r >= groups) ++q, r -= groups;
   }
   __device__ __forceinline__ int begin(int s) const {
-    return s * q + (int)((unsigned)(s * r) / (unsigned)groups);
+    return s * q + (int)__umulhi((uint32_t)(s * r), inv);  // exact: s r groups < 2^32
   }
   // the group that has place u
   __device__ __forceinline__ int group_of(int u) const {
-    const uint64_t x = (uint64_t)(u + 1) * groups - 1;
-    return x >> 32 ? (int)(x / (unsigned)W) : (int)((unsigned)x / (unsigned)W);
+    int s = min(groups - 1, (int)(((float)u + 1.f) * (float)groups / (float)W));  // at most one off
+    if (begin(s) > u) --s;
+    else if (begin(s + 1) <= u) ++s;
+    return s;
   }
 };
 
@@ -117,10 +130,13 @@ __device__ __forceinline__ bool next_share(const AttnParams& p, const Line& line
       if (line.prefix[mid] <= u) lo = mid;
       else hi = mid;
     }
-    const int places = (line.prefix[lo + 1] - line.prefix[lo]) / p.cache.n_kv;
     s.b = lo;
+    const int places = (line.prefix[lo + 1] - line.prefix[lo]) / p.cache.n_kv, at = u - line.prefix[lo];
     s.nt = places - p.extra;
-    s.g = (u - line.prefix[lo]) / places;
+    // floor(at / places), which is below 4096: the rounded quotient is at most one off
+    s.g = (int)__fdividef((float)at, (float)places);
+    if (s.g * places > at) --s.g;
+    else if ((s.g + 1) * places <= at) ++s.g;
     const int tile0 = line.prefix[lo] + s.g * places + p.extra;  // place of the item's tile 0
     s.k0 = max(u - tile0, 0);
     s.n = min(u_end - tile0, s.nt) - s.k0;

@@ -1023,7 +1023,7 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  const Cut cut(line.prefix[p.B], p.groups);
+  const Cut cut(line.prefix[p.B], p);
   const int u_begin = cut.begin(group), u_end = cut.begin(group + 1);
 
   // Registers: 16 warps launched with 128 each, 8 x 184 + 8 x 72 is the
