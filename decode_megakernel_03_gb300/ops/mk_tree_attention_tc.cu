@@ -34,10 +34,10 @@
 // V by columns.
 //
 // Measured, 8 sequences over 16384 keys each, 8B shape (537 MB): bf16 with 64 rows 96
-// us, 5.6 TB/s, bound by the bytes; with 256 rows 128 us, 4.3 TB/s and 1.08 PFLOP/s,
+// us, 5.6 TB/s, bound by the bytes; with 256 rows 125 us, 4.4 TB/s and 1.11 PFLOP/s,
 // bound by the chain from a tile's scores through their softmax and weights to the
 // next scores (3150 cycles a tile, 2000 of them softmax, two tiles in flight);
-// fp32 with 32 rows 111 us, with 256 rows 259 us (in bf16 parts 1.6 PFLOP/s).
+// fp32 with 32 rows 110 us, with 256 rows 259 us (in bf16 parts 1.6 PFLOP/s).
 //
 // Every wait ends: after kWaitNs a thread stops waiting for good and goes on, and
 // the rows of the block come out as NaN.
