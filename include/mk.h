@@ -433,7 +433,8 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
    heads per kv-head; n_tokens 1 to MK_MAX_TREE. Softmax of scale * (q . k) in
    fp32. A row that sees no key is 0; NaN and infinities in rows it does not
    see do not reach it. out may be q (with q's stride). Deterministic: the same
-   inputs give the same bits.
+   inputs give the same bits. (Should a wait inside the kernel run out, after 2
+   s, it returns all the same and the rows in question are NaN.)
    Errors: MK_ERR_INVALID (also a workspace below the query's size),
    MK_ERR_CUDA. */
 int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
