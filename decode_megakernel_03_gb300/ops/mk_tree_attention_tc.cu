@@ -118,8 +118,12 @@ __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() {
+// Waits for the loads; r (n of what they load) is not to be used before.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -589,7 +593,7 @@ __device__ __forceinline__ float read_scores(uint32_t at, bool some, const uint3
                                              uint32_t (&x)[N]) {
 #pragma unroll
   for (int h = 0; h < N / 32; ++h) tmem_load32(at + 32 * h, x + 32 * h);
-  tmem_wait_ld();
+  tmem_wait_ld<N>(x);
   if (some) {
 #pragma unroll
     for (int e = 0; e < N; ++e)
@@ -749,7 +753,7 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
             tmem_load32(t_o + c, o);
-            tmem_wait_ld();
+            tmem_wait_ld<32>(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
             tmem_store32(t_o + c, o);
@@ -816,12 +820,12 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
         uint32_t o[32];
         float y[32];
         tmem_load32(t_o + c, o);
-        tmem_wait_ld();
+        tmem_wait_ld<32>(o);
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
         if (second) {
           tmem_load32(t_o + D + c, o);
-          tmem_wait_ld();
+          tmem_wait_ld<32>(o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] += f1 != 0.f ? __uint_as_float(o[e]) * f1 : 0.f;
         }
@@ -939,7 +943,7 @@ __device__ __forceinline__ void exact_role(const AttnParams& p, Shared& sm, cons
           for (int c = 0; c < D / 2; c += 32) {
             uint32_t y[32];
             tmem_load32(t_o + t * D + c, y);
-            tmem_wait_ld();
+            tmem_wait_ld<32>(y);
 #pragma unroll
             for (int e = 0; e < 32; ++e) acc[c + e] = fmaf(acc[c + e], last_keep, __uint_as_float(y[e]));
           }
