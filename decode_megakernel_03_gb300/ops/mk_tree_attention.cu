@@ -30,10 +30,9 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 // ---- the kernel ------------------------------------------------------------------------
 // One m16 block of rows. P = 1: bf16 activations; P = 3: fp32 ones, queries and
 // weights as three bf16 parts (2^-24 of the value: fp32's own step; the cache is
-// bf16, so products of parts are exact). Weights of bf16 calls are rounded to
-// bf16 (relative 2^-8, the size of the output's own rounding); sums, maxima and
-// the output accumulate in fp32. A tile is 16 KB of keys and 16 KB of values
-// whatever the head's size: 64-key tiles of 64 dimensions spent their time on the
+// bf16, so products of parts are exact). Weights of bf16 calls are two bf16 parts
+// (2^-17, as the decode step holds its own); sums, maxima and the output accumulate
+// in fp32. A tile is 16 KB of keys and 16 KB of values whatever the head's size: 64-key tiles of 64 dimensions spent their time on the
 // barriers between them. Three tiles per block and two blocks per SM keep 192 KB
 // per SM in flight. Bound by the bytes of the keys and values: a single bf16 token of
 // 8 sequences over 16384 keys each (8B shape, 537 MB) takes 88 us, 6.1 TB/s; fp32 in
@@ -59,6 +58,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 tree_attention_kernel(const __grid_constant__ AttnParams p) {
   using Lay = Layout<D, P>;
   constexpr int kTile = Lay::kTile, RT = kRows, KB = D / 16, NB = D / 8;
+  constexpr int W = P == 1 ? 2 : P;  // parts of the weights
   constexpr int NK = kTile / 64;  // blocks of 16 keys that a warp takes of a tile
   extern __shared__ __align__(1024) uint8_t smem[];
   uint32_t* rowtab = reinterpret_cast<uint32_t*>(smem + Lay::kRing);  // [kStages + 1][kTile]
@@ -329,21 +329,24 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
       // o += weights x v
 #pragma unroll
       for (int nk = 0; nk < NK; ++nk) {
-        uint4 w[P];
-        uint32_t part[4][P];
+        uint4 w[W];
+        uint32_t part[4][W];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           split(s[nk][j / 2][j % 2 * 2], s[nk][j / 2][j % 2 * 2 + 1], part[j]);
 #pragma unroll
-        for (int q = 0; q < P; ++q) w[q] = make_uint4(part[0][q], part[1][q], part[2][q], part[3][q]);
+        for (int q = 0; q < W; ++q) w[q] = make_uint4(part[0][q], part[1][q], part[2][q], part[3][q]);
 #pragma unroll
         for (int d = 0; d < NB; d += 2) {
           const int r = (warp * NK + nk) * 16 + (lane / 8) % 2 * 8 + lane % 8, c = d + lane / 16;
           uint32_t vf[4];
           ldsm_x4_t(vf, vs + r * (D * 2) + ((c ^ (r & 7)) * 16));
           if constexpr (P == 1) {
-            mma_bf16_16816(o[d], w[0], vf[0], vf[1]);
-            mma_bf16_16816(o[d + 1], w[0], vf[2], vf[3]);
+#pragma unroll
+            for (int q = W - 1; q >= 0; --q) {
+              mma_bf16_16816(o[d], w[q], vf[0], vf[1]);
+              mma_bf16_16816(o[d + 1], w[q], vf[2], vf[3]);
+            }
           } else {
             float x[2][4] = {};
 #pragma unroll

@@ -11,11 +11,12 @@
 // parity s, and stream 0 joins the two at the end. Either way one stream's
 // softmax runs while the matrix unit works for the other. Per stream and tile:
 // S = Q K^T (128 x 128, fp32, tensor memory); the row's thread reads it, masks
-// it, and writes the weights p = 2^(s - m) back as bf16 over S; O += P V (128 x D,
-// fp32, tensor memory). The reference m of a row follows its maximum only when
-// that exceeds it by 2^8 (or at the first key), so O is almost never rescaled;
-// the sum of the weights is kept in fp32 from the unrounded weights. The
-// weights' rounding to bf16 (relative 2^-8) is the size of the output's own.
+// it, and writes the weights p = 2^(s - m) back over S as two bf16 parts, which are
+// p to 2^-16 (as the decode step holds its own; with one part, 2^-9, the output
+// was 1.2 to 1.4 times as far from 64 bits as its rounding); O += P V (128 x D, fp32,
+// tensor memory), once per part. The reference m of a row follows its maximum
+// only when that exceeds it by 2^8 (or at the first key), so O is almost never
+// rescaled; the sum of the weights is kept in fp32 from the unrounded weights.
 //
 // fp32 activations. Queries and weights go in as three bf16 parts (2^-24 of the
 // value), each product runs once per part; up to 32 rows stand three times in the
@@ -104,14 +105,6 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
@@ -191,16 +184,17 @@ enum { kOne, kTwo, kExact, kFew };
 
 constexpr int kKeys = 128;  // keys of a tile
 
-// Columns of tensor memory (512): kOne, kTwo: scores (weights over them) of stream
-// s at 128 s, its output at 256 + D s. kExact: scores of tile parity s, the three
-// parts of the weights over them, at 192 s, a tile's product at 384. kFew: scores
-// (weights over them) of tile parity s at 128 s, the tile's product at 256 + D s.
+// Columns of tensor memory (512): kOne, kTwo: scores (the two parts of the weights
+// over them) of stream s at 128 s, its output at 256 + D s. kExact: scores of tile
+// parity s, the three parts of the weights over them, at 192 s, a tile's product at
+// 384. kFew: scores (weights over them) of tile parity s at 128 s, the tile's
+// product at 256 + D s.
 template <int D, int KIND>
 struct Layout {
   static constexpr bool TWO = KIND == kTwo;
   static constexpr bool EXACT = KIND == kExact || KIND == kFew;
   static constexpr int PARTS = EXACT ? 3 : 1;             // of the queries
-  static constexpr int WEIGHT_PARTS = KIND == kExact ? 3 : 1;  // one after another
+  static constexpr int WEIGHT_PARTS = KIND == kExact ? 3 : KIND == kFew ? 1 : 2;  // one after another
   static constexpr int PRODUCTS = KIND == kExact ? 1 : 2;      // outputs or products
   static constexpr int kScoreStep = KIND == kExact ? 192 : 128;
   static constexpr int kOut = 2 * kScoreStep;
@@ -452,19 +446,16 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
     fence_async_smem();
     tc_fence_after();
     if constexpr (TWO) {
-      uint32_t at = take();
-      scores(0, at, false);
-      scores(1, at, true);
-      for (int j = 0; j < sh.n; ++j) {
-        const bool more = j + 1 < sh.n;
-        const uint32_t v_at = take();
-        values(0, v_at, j > 0, false);
-        if (more) {
-          at = take();
-          scores(0, at, false);
+      uint32_t k_at = take(), v_at = 0;
+#pragma unroll 1
+      for (int i = -2; i < 2 * sh.n; ++i) {  // stream i & 1: products of tile i / 2, then the next scores
+        const int s = i & 1;
+        if (i >= 0) {
+          if (s == 0) v_at = take();
+          values(s, v_at, i >= 2, s == 1);
+          if (s == 0 && i + 2 < 2 * sh.n) k_at = take();
         }
-        values(1, v_at, j > 0, true);
-        if (more) scores(1, at, true);
+        if (i + 2 < 2 * sh.n) scores(s, k_at, s == 1);
       }
     } else {
       for (int s = 0; s < 2 && s < sh.n; ++s) scores(s, take(), true);
@@ -630,7 +621,7 @@ __device__ __forceinline__ float2 weights2(uint32_t a, uint32_t b, unsigned long
   return w;
 }
 
-// Part q of two weights (finite, not negative), as bf16: the upper 8 bits of the
+// Part q of two weights (not negative; a NaN stays one), as bf16: the upper 8 bits of the
 // significand, the next 8, the last 8, so that the three parts' sum is the weight.
 template <int q>
 __device__ __forceinline__ uint32_t weight_part(float2 w) {
@@ -643,6 +634,15 @@ __device__ __forceinline__ uint32_t weight_part(float2 w) {
     x = __float_as_uint(z.x), y = __float_as_uint(z.y);
   }
   return __byte_perm(x, y, 0x7632);  // the upper halves
+}
+// What part 0 leaves of two weights, rounded to bf16: with part 0 the weight to
+// 2^-16 of it.
+__device__ __forceinline__ uint32_t weight_rest(float2 w) {
+  const uint32_t x = __float_as_uint(w.x), y = __float_as_uint(w.y);
+  unsigned long long rest = pack2(w.x, w.y);
+  add2(rest, pack2(-__uint_as_float(x & 0xffff0000u), -__uint_as_float(y & 0xffff0000u)));
+  const float2 z = unpack2(rest);
+  return bf16x2_rn(z.x, z.y);
 }
 
 // 32 columns of a finished row: the odd values it sees added, then written out
@@ -764,15 +764,17 @@ __device__ __forceinline__ void softmax_role(const AttnParams& p, Shared& sm, co
         unsigned long long sums[2] = {0, 0};
         __syncwarp();
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t w[16];
+        for (int h = 0; h < 8; ++h) {
+          uint32_t w[2][8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 a = weights2(x[32 * h + 2 * e], x[32 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
-            w[e] = bf16x2_rn(a.x, a.y);
+          for (int e = 0; e < 8; ++e) {
+            const float2 a = weights2(x[16 * h + 2 * e], x[16 * h + 2 * e + 1], scale2, from2, sums[e % 2]);
+            w[0][e] = weight_part<0>(a);
+            w[1][e] = weight_rest(a);
           }
-          tmem_store16(t_s + 16 * h, w);
-          if (h == 1) {  // its products need not wait for the second half
+          tmem_store8(t_s + 8 * h, w[0]);
+          tmem_store8(t_s + 64 + 8 * h, w[1]);
+          if (h == 3) {  // its products need not wait for the second half
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
