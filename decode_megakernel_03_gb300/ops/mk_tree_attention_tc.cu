@@ -303,6 +303,10 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
 
     for (int j = -LEAD; j < sh.n; ++j) {
       if (j >= 0) {
+        // the share's list of odd values is free again (the share before last is
+        // written). For every share, whether it has odd values or not: a parity tells
+        // only neighbouring phases apart, so none may be passed over.
+        if (j == 0 && share >= 2) wait(&sm.done[share & 1], share / 2 - 1);
         wait(&sm.empty[buf], round + 1);
         const uint32_t rows = held[0];
         copy(p.v, rows);
@@ -312,7 +316,6 @@ __device__ __forceinline__ void load_role(const AttnParams& p, Shared& sm, const
           // cancelled by a zero weight if it is not finite, so it is taken out
           // here and added at the end to the rows that see it
           asm volatile("cp.async.wait_all;" ::: "memory");
-          if (share >= 2) wait(&sm.done[share & 1], share / 2 - 1);  // its list is free again
           __syncwarp();
           uint8_t* base = ring_ptr + buf * Lay::kBuf + (c / 8) * (kKeys * 128);
           for (int i = 0; i < kLoadRows / RPW; ++i) {
