@@ -40,8 +40,9 @@
 // next scores (3150 cycles a tile, 2000 of them softmax, two tiles in flight);
 // fp32 with 32 rows 110 us, with 256 rows 259 us (in bf16 parts 1.6 PFLOP/s).
 //
-// Every wait ends: after kWaitNs a thread stops waiting for good and goes on, and
-// the rows of the block come out as NaN.
+// Every wait ends: after kWaitNs and a last try of kLastTryNs a thread stops waiting
+// for good and goes on, the rows of the block come out as NaN, and the block ends
+// when its copies and products in flight have.
 #include <type_traits>
 
 #include "mk_tree_attention.cuh"
@@ -54,6 +55,9 @@ constexpr int kThreads = 512;
 
 constexpr int kMasks = 8;           // tiles whose masks are kept
 constexpr uint64_t kWaitNs = 2000000000ull;
+// The clock goes on while a block is off its SM (another process's turn), and what
+// the block waits for went no further either: time for that behind the limit.
+constexpr uint32_t kLastTryNs = 20000000;
 constexpr float kSlack = 8.f;       // log2 of how far a weight may exceed 1
 
 // ---- tensor memory and the matrix unit -------------------------------------------
@@ -209,6 +213,7 @@ struct Shared {
   uint64_t s_full[2];              // a stream's scores are in tensor memory
   uint64_t p_full[2][2];           // the weights of a stream's first, last 64 keys are
   uint64_t q_full, o_full;         // a share's queries are loaded / its products done
+  uint64_t drained;                // every product of the block is done
   uint64_t done[2];                // a share (by parity) is written
   uint32_t tmem;
   int failed;                      // a wait ran out
@@ -224,6 +229,19 @@ struct Shared {
   float top[2][2][128], sum[2][128];
 };
 
+// mbar_try_wait that may suspend the thread for up to about `ns`
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return done != 0;
+}
+
 // Waits with an end: a thread whose wait ran out does not wait again (its
 // control flow goes on unchanged, so that barriers keep their counts).
 struct Waiter {
@@ -234,7 +252,7 @@ struct Waiter {
     if (!ok || mbar_try_wait(bar, parity & 1)) return;
     const uint64_t since = globaltimer();
     while (!mbar_try_wait(bar, parity & 1)) {
-      if (globaltimer() - since > kWaitNs) {
+      if (globaltimer() - since > kWaitNs && !mbar_try_wait_for(bar, parity & 1, kLastTryNs)) {
         ok = false;
         *reinterpret_cast<volatile int*>(&sm.failed) = 1;
         return;
@@ -475,6 +493,13 @@ __device__ __forceinline__ void mma_role(const AttnParams& p, Shared& sm, const 
     __syncwarp();
     ++share;
   }
+  // Products may be in flight yet where a wait ran out (else the rows' threads have
+  // waited for them): the tensor memory is given back behind them. The wait runs
+  // beside the writing of the last rows.
+  if (elect_one()) tc_commit(&sm.drained);
+  __syncwarp();
+  Waiter last(sm);
+  last(&sm.drained, 0);
 }
 
 // ---- the softmax warps -------------------------------------------------------------------
@@ -1023,6 +1048,7 @@ tree_attention_tc_kernel(const __grid_constant__ AttnParams p) {
     }
     mbar_init(&sm.q_full, kSoftWarps);
     mbar_init(&sm.o_full, 2);
+    mbar_init(&sm.drained, 1);
     sm.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
