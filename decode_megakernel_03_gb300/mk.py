@@ -11,7 +11,6 @@ import ctypes
 import os
 
 import numpy as np
-import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmk.so")
@@ -476,6 +475,7 @@ class Cache:
     """
 
     def __init__(self, k: list, v: list, block_table=None):
+        _use_torch()
         k, v = list(k), list(v)
         if not k or len(k) != len(v):
             raise _bad("k and v must hold a tensor for each layer")
@@ -528,11 +528,23 @@ class Rope:
         _check(lib().mk_rope_init(ctypes.byref(cfg), self.ref))
 
 
-# the current stream's handle and device without making objects (a few
-# microseconds less per call), where this torch has the short ways
-_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+torch = None  # see _use_torch
+
+
+def _use_torch():
+    """Imports torch where the first tensor comes in (schedules, page tables and
+    rotary plans need none)."""
+    global torch, _TYPES, _current_raw, _current_device
+    if torch is not None:
+        return
+    import torch as t
+    _TYPES = {t.bfloat16: TYPE_BF16, t.float32: TYPE_FP32}
+    # the current stream's handle and device without making objects (a few
+    # microseconds less per call), where this torch has the short ways
+    _current_raw = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: t.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    torch = t
 
 
 def _elsewhere(device, stream):
@@ -556,9 +568,6 @@ def _ints(t, device, what: str, shape):
     if t.shape != shape:
         raise _bad(f"{what} has the shape {tuple(t.shape)}, not {shape}")
     return t.data_ptr()
-
-
-_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_FP32}
 
 
 def _type_of(t, what: str) -> int:
@@ -656,6 +665,7 @@ def tree_attention(cache: Cache, layer: int, q, starts, parents=None, counts=Non
 def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     """mk_tree_accept: logits [B][T][V] (bf16 or fp32), tokens [B][T] int32.
     Returns int32 (choices [B][T], path [B][T], accepted [B], next [B])."""
+    _use_torch()
     dev, shape = logits.device, logits.shape
     if not logits.is_cuda or len(shape) != 3:
         raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
