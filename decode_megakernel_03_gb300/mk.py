@@ -80,8 +80,8 @@ class MkCache(ctypes.Structure):
 class MkRopeConfig(ctypes.Structure):
     _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int),
                 ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
-                ("theta", ctypes.c_float), ("factor", ctypes.c_float), ("low", ctypes.c_float),
-                ("high", ctypes.c_float), ("original_length", ctypes.c_int),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("original_length", ctypes.c_int),
                 ("magnitude", ctypes.c_float)]
 
 

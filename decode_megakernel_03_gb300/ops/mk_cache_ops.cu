@@ -129,13 +129,14 @@ struct RopeParams {
 };
 
 // A block takes `tokens` rows: one angle per (token, pair), shared by all heads
-// (sincospif of a fraction of a turn found by a 64-bit fixed-point product, so
-// that it is exact to 2^-64 turns at any position). Then a warp takes heads of q,
-// k and v of one row, D / 8 lanes to a head. A lane has four pairs, both members
-// of each, so that its sines and cosines stay in its registers and nothing is
-// exchanged (q_out may be q). PIECE: elements that lie together for a lane, 8 when
-// the pairs are neighbours, else the largest of 4, 2, 1 that divides
-// rotary_dim / 2; the elements behind rotary_dim are taken as neighbours.
+// (sincospif of a fraction of a turn found by a 64-bit fixed-point product: position
+// times the plan's own 2^-53 turns off, less than fp32's rounding up to position 2^27).
+// Then a warp takes heads of q, k and v of one row, D / 8 lanes to a head. A lane
+// has four pairs, both members of each, so that its sines and cosines stay in its
+// registers and nothing is exchanged (q_out may be q). PIECE: elements that lie
+// together for a lane, 8 when the pairs are neighbours, else the largest of 4, 2, 1
+// that divides rotary_dim / 2; the elements behind rotary_dim are taken as
+// neighbours.
 // (Eight elements in a row per lane and the partners by shuffles: 218 us
 // against 132 for the 32768 rows below in halves of 64, 450 against 138 in
 // halves of 62, where the partners were loaded one by one.)
@@ -431,23 +432,23 @@ int mk_rope_init(const mk_rope_config* c, mk_rope* out) {
   const int n = c->rotary_dim;
   if (n < 2 || n > c->head_dim || n % 2)
     return op_fail(MK_ERR_INVALID, "rope: rotary_dim must be even, 2 to head_dim");
-  if (!(c->theta >= 1.f) || !(c->factor >= 1.f) || std::isinf(c->theta) || std::isinf(c->factor))
+  if (!(c->theta >= 1) || !(c->factor >= 1) || std::isinf(c->theta) || std::isinf(c->factor))
     return op_fail(MK_ERR_INVALID, "rope: theta and factor must be at least 1 and finite");
   if (c->scaling < MK_ROPE_NONE || c->scaling > MK_ROPE_YARN ||
       (c->interleaved != 0 && c->interleaved != 1))
     return op_fail(MK_ERR_INVALID, "rope: unknown scaling or layout");
   const bool by_length = c->scaling == MK_ROPE_BANDS || c->scaling == MK_ROPE_YARN;
-  if (by_length && (c->original_length < 1 || !(c->low > 0.f) || !(c->high > c->low) ||
+  if (by_length && (c->original_length < 1 || !(c->low > 0) || !(c->high > c->low) ||
                     std::isinf(c->high)))
     return op_fail(MK_ERR_INVALID, "rope: original_length >= 1 and 0 < low < high are needed");
-  if (c->scaling == MK_ROPE_YARN && !(c->theta > 1.f))
+  if (c->scaling == MK_ROPE_YARN && !(c->theta > 1))
     return op_fail(MK_ERR_INVALID, "rope: MK_ROPE_YARN needs theta above 1");
   if (!(c->magnitude >= 0.f) || std::isinf(c->magnitude))
     return op_fail(MK_ERR_INVALID, "rope: magnitude must be finite and not negative");
   const double two_pi = 6.283185307179586476925, length = c->original_length;
   double first = 0, last = 0;  // MK_ROPE_YARN: the ramp over the pairs
   if (c->scaling == MK_ROPE_YARN) {
-    const double per = n / (2 * std::log((double)c->theta));
+    const double per = n / (2 * std::log(c->theta));
     first = std::floor(per * std::log(length / (c->high * two_pi)));
     last = std::ceil(per * std::log(length / (c->low * two_pi)));
     if (first < 0) first = 0;
@@ -457,16 +458,16 @@ int mk_rope_init(const mk_rope_config* c, mk_rope* out) {
   out->rotary_dim = n;
   out->interleaved = c->interleaved;
   out->magnitude = c->magnitude > 0.f ? c->magnitude
-                   : c->scaling == MK_ROPE_YARN ? (float)(0.1 * std::log((double)c->factor) + 1)
+                   : c->scaling == MK_ROPE_YARN ? (float)(0.1 * std::log(c->factor) + 1)
                                                 : 1.f;
   for (int i = 0; i < 64; ++i) out->turns[i] = 0;
   for (int i = 0; i < n / 2; ++i) {
-    double f = std::pow((double)c->theta, -2.0 * i / n);
+    double f = std::pow(c->theta, -2.0 * i / n);
     const double far = f / c->factor;
     if (c->scaling == MK_ROPE_LINEAR) {
       f = far;
     } else if (c->scaling == MK_ROPE_BANDS) {
-      const double mix = (length * f / two_pi - c->low) / ((double)c->high - c->low);
+      const double mix = (length * f / two_pi - c->low) / (c->high - c->low);
       f = mix <= 0 ? far : mix >= 1 ? f : (1 - mix) * far + mix * f;
     } else if (c->scaling == MK_ROPE_YARN) {
       const double ramp = last > first ? (i - first) / (last - first) : i > first ? 1.0 : 0.0;

@@ -397,7 +397,7 @@ typedef struct {
 typedef struct {
   int head_dim, rotary_dim; /* rotary_dim even, 2 to head_dim */
   int interleaved, scaling;
-  float theta, factor, low, high; /* theta >= 1, factor >= 1 */
+  double theta, factor, low, high; /* theta >= 1, factor >= 1 */
   int original_length;      /* MK_ROPE_BANDS, MK_ROPE_YARN */
   float magnitude;          /* 0: 1, or 0.1 ln(factor) + 1 for MK_ROPE_YARN */
 } mk_rope_config;
@@ -406,7 +406,9 @@ typedef struct {
 typedef struct {
   int head_dim, rotary_dim, interleaved;
   float magnitude;
-  uint64_t turns[64]; /* f_i / (2 pi) in units of 2^-64 turns */
+  uint64_t turns[64]; /* f_i / (2 pi) in units of 2^-64 turns, to 2^-53 turns: an angle is
+                         off by position * 2^-53 turns at most beside its fp32 rounding
+                         (2^-26), less than that up to position 2^27 */
 } mk_rope;
 
 /* Host only. MK_ERR_INVALID when a member is out of its range. */
