@@ -385,7 +385,11 @@ typedef struct {
    others pass through) turns by position * f_i, f_i = theta^(-2i / rotary_dim)
    scaled as `scaling` says, and is multiplied by `magnitude`.
    interleaved 0: pair i is (i, i + rotary_dim / 2), as the decode step has it;
-   1: (2i, 2i + 1). */
+   1: (2i, 2i + 1).
+   mk_decode_step and the other calls with a handle know one plan: the whole head in
+   halves with the handle's rope_theta, unscaled. They can go on from rows that
+   mk_rope_append wrote with that plan; a cache of any other plan is read and
+   continued by the calls below only (the library cannot tell). */
 #define MK_ROPE_NONE 0
 #define MK_ROPE_LINEAR 1 /* f / factor */
 #define MK_ROPE_BANDS 2  /* by the turns n = original_length f / (2 pi): below
@@ -433,10 +437,14 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
    cache already: mk_rope_append). q, out: DEVICE `type`, rows as above
    ([n_heads][head_dim]); n_heads a multiple of n_kv_heads, at most 8 query
    heads per kv-head; n_tokens 1 to MK_MAX_TREE. Softmax of scale * (q . k) in
-   fp32. A row that sees no key is 0; NaN and infinities in rows it does not
-   see do not reach it. out may be q (with q's stride). Deterministic: the same
+   fp32; its weights enter the product with the values as bf16 parts that hold them
+   to 2^-16 (fp32 calls: weights and queries to 2^-24). A row that sees no key is 0;
+   NaN and infinities in rows it does not see do not reach it. Infinities that it does
+   see in keys or in the context's values may make it NaN where the formula gives
+   an infinity or a weight of 0. out may be q (with q's stride). Deterministic: the same
    inputs give the same bits. (Should a wait inside the kernel run out, after 2
-   s, it returns all the same and the rows in question are NaN.)
+   s, it returns all the same and the rows in question are NaN. A process that is
+   kept off the GPU for longer than that may meet this in a sound call.)
    Errors: MK_ERR_INVALID (also a workspace below the query's size),
    MK_ERR_CUDA. */
 int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
@@ -468,8 +476,9 @@ int mk_tree_accept_workspace(int batch, int n_tokens, int vocab, size_t* bytes);
 
 /* Moves the accepted rows down behind the context, in every layer, K and V:
    row starts[b] + i <- row starts[b] + path[b][i] for i < accepted[b] (DEVICE
-   int32 arrays as mk_tree_accept writes them). Entries that do not ascend,
-   or lie outside [i, n_tokens), are skipped. Errors: MK_ERR_INVALID,
+   int32 arrays as mk_tree_accept writes them; n_tokens 1 to MK_MAX_TREE: the path
+   of a longer chain is 0, 1, 2, ..., which moves nothing). Entries that do not
+   ascend, or lie outside [i, n_tokens), are skipped. Errors: MK_ERR_INVALID,
    MK_ERR_CUDA. */
 int mk_cache_compact(const mk_cache* cache, int batch, int n_tokens, const int32_t* starts,
                      const int32_t* path, const int32_t* accepted, void* stream);
