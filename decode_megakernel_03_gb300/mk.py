@@ -492,7 +492,7 @@ class Cache:
         self.batch, entries, ptr = self.n_blocks, 0, None
         if block_table is not None:
             # (an empty table has no pointer, which would read as a contiguous cache)
-            if len(block_table.shape) != 2 or block_table.numel() == 0:
+            if len(block_table.shape) != 2 or 0 in block_table.shape:
                 raise _bad("block_table must be [batch][entries], at least one of each")
             ptr = _ints(block_table, self.device, "block_table", block_table.shape)
             self.batch, entries = map(int, block_table.shape)
