@@ -294,8 +294,9 @@ struct MoveParams {
 // (row numbers at kv-head 0) once in shared memory, then each thread moves its
 // 16-byte column of every row. Sources ascend and no source lies below its
 // destination, so loading eight rows before storing them never meets a row
-// that an earlier store has overwritten. Bound by latency, the rows are few: six
-// rows of 8 sequences in 16 layers of the 1B shape, 1.6 MB, take 3.8 us.
+// that an earlier store has overwritten. Bound by latency, the rows are few: one to
+// six accepted rows of 8 sequences in 16 layers of the 1B shape, 24 of them to move,
+// 1.6 MB, take 3.8 us.
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ MoveParams p) {
   __shared__ uint32_t from[MK_MAX_TREE], to[MK_MAX_TREE];

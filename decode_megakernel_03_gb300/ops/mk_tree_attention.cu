@@ -35,10 +35,10 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 // in fp32. A tile is 16 KB of keys and 16 KB of values whatever the head's size: 64-key tiles of 64 dimensions spent their time on the
 // barriers between them. Three tiles per block and two blocks per SM keep 192 KB
 // per SM in flight. Bound by the bytes of the keys and values: a single bf16 token of
-// 8 sequences over 16384 keys each (8B shape, 537 MB) takes 88 us, 6.1 TB/s; fp32 in
-// heads of 64 (1B shape, 268 MB) 71 us, bound by its six products and the
+// 8 sequences over 16384 keys each (8B shape, 537 MB) takes 89 us, 6.0 TB/s; fp32 in
+// heads of 64 (1B shape, 268 MB) 70 us, bound by its six products and the
 // splitting. Short contexts are bound by
-// latency: 512 keys of one sequence 9.1 us, two launches of which the second
+// latency: 512 keys of one sequence 9.2 us, two launches of which the second
 // waits for the first inside.
 constexpr int tile_keys(int D) { return 8192 / D; }
 
@@ -564,28 +564,31 @@ struct Plan {
 // that take turns at the key tiles), fp32 ones in tiles of 128 rows, or, up to 32
 // rows, with the parts of the weights stacked.
 // Warp-level against tensor-memory kernel, us:
-//   8 sequences over 16384 keys, 8B shape, bf16   4 nodes (16 rows)  93.2    93.5
-//                                                 5 nodes (20 rows) 147.6    94.2
-//                                          fp32   1 node            133.7   103.9
-//                                                 4 nodes           140.0   107.0
-//                                1B shape, fp32   4 nodes            72.1    82.0
-//   8 sequences over 1024 keys,  8B shape, fp32   1 node             21.8    24.4
-//                                                 4 nodes            26.7    27.7
-//   one sequence over 1024 keys, 8B shape, bf16   1 node             11.3    13.3
-//                                                 5 nodes            14.3    14.0
-//   4 sequences over 4096 keys,  1B shape, fp32   4 nodes            18.5    22.6
+//   8 sequences over 16384 keys, 8B shape, bf16   4 nodes (16 rows)  93.2    93.4
+//                                                 5 nodes (20 rows) 159.6    92.7
+//                                          fp32   1 node            129.9   103.3
+//                                                 4 nodes           136.9   107.6
+//                                1B shape, fp32   4 nodes            70.8    82.0
+//   8 sequences over 1024 keys,  8B shape, fp32   1 node             22.0    23.9
+//                                                 4 nodes            26.3    26.8
+//   one sequence over 1024 keys, 8B shape, bf16   1 node             10.6    12.7
+//                                                 5 nodes            13.7    13.6
+//   4 sequences over 4096 keys,  1B shape, fp32   4 nodes            18.9    21.9
 // fp32 parts stacked against one after another (8 sequences over 16384 keys, 8 nodes): 8B
-// shape 111 us against 129, 1B shape 83 against 94.
+// shape 111 us against 129, 1B shape 84 against 94.
 // Two blocks of up to 128 rows in a pass over the keys against a pass for each (bf16,
-// 8 sequences over 16384 keys): 132 rows 112 us against 132, 256 rows 128 against
-// 141; the lengths are not known here, and one sequence over 2048 keys, where the
-// second block's share only adds to the first's, takes 31 us against 27.
+// 8 sequences, 8B shape), 132 / 256 rows: over 16384 keys 154 / 168 us against 165 /
+// 170, over 32768 285 / 315 against 308 / 325, over 4096 59 / 68 against 62 / 65; the
+// lengths are not known here, and one sequence over 2048 keys, where the second
+// block's share only adds to the first's, takes 27 / 30 us against 23 / 24.
 Plan plan_of(int T, int G, int D, int type, int n_sm) {
   Plan pl;
   const int rows = T * G;
   pl.tc = rows > kRows || (type == MK_TYPE_FP32 && D == 128);
-  // measured at 0 to 8: 25 nodes over 128 to 4096 keys (1B shape, 8 sequences) 32.8 us
-  // at 0, 25.2 at 2, 23.1 at 4, 24.2 at 8; the other cases within 2 % from 2 to 8
+  // measured at 0, 2, 4 and 8: 25 nodes over 128 to 4096 keys (1B shape, 8 sequences)
+  // 32.4, 24.1, 22.9, 24.0 us; 6 fp32 nodes over 2048 to 16384 keys (8B shape, 4
+  // sequences) 51.3, 49.5, 46.6, 45.4; one token of 64 sequences over 1024 keys (1B
+  // shape) 39.6, 40.4, 42.5, 43.4; one sequence over 4096 keys alike within 5 %
   pl.extra = 4;
   if (pl.tc && type == MK_TYPE_FP32) {
     pl.tile = 128;
@@ -658,8 +661,8 @@ int launch_all(const AttnParams& p, const Plan& pl, int type, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // A block for a row where that still leaves few blocks per SM (1B shape over
-  // 4096 keys, rows of all kv-heads: 32 rows 13.5 us against 21.5, 512 14.4 against
-  // 17.3, 1024 15.9 against 17.4, but 2048 21.5 against 19.5, 4096 28.7 against 22.1)
+  // 4096 keys, rows of all kv-heads: 32 rows 13.3 us against 20.3, 512 13.8 against
+  // 18.3, 1024 15.6 against 20.0; 2048 21.7 against 22.8, but 4096 29.7 against 23.8)
   const bool few = (int64_t)p.T * p.G * p.B * p.cache.n_kv <= 1024;
   cfg.gridDim = dim3(few ? p.T * p.G : (p.T * p.G + 3) / 4, p.B * p.cache.n_kv);
   cfg.blockDim = dim3(128);

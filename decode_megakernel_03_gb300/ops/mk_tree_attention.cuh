@@ -43,8 +43,8 @@ struct AttnParams {
 // ---- the line of work -----------------------------------------------------------
 // Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), each is
 // `extra` places and then its tiles in order. A block finds its part of the line
-// before it can fetch anything, so that this part has one division left (five took
-// 1000 of the 5000 cycles before the first copy).
+// before it can fetch anything, so that this part has one division left (with five a
+// block's start took 1000 cycles longer).
 
 // The line in shared memory: the places of the sequences before b, and the
 // sequences' starts and counts (at their bounds).

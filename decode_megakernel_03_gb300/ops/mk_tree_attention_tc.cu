@@ -34,11 +34,13 @@
 // lie in the 128-byte-swizzled form in which the matrix unit reads K by rows and
 // V by columns.
 //
-// Measured, 8 sequences over 16384 keys each, 8B shape (537 MB): bf16 with 64 rows 96
-// us, 5.6 TB/s, bound by the bytes; with 256 rows 125 us, 4.4 TB/s and 1.11 PFLOP/s,
-// bound by the chain from a tile's scores through their softmax and weights to the
-// next scores (3150 cycles a tile, 2000 of them softmax, two tiles in flight);
-// fp32 with 32 rows 110 us, with 256 rows 259 us (in bf16 parts 1.6 PFLOP/s).
+// Measured, 8 sequences over 16384 keys each, 8B shape (537 MB): bf16 with 64 rows 98
+// us, 5.5 TB/s, bound by the bytes; with 256 rows 168 us, 3.2 TB/s and 1.23 PFLOP/s of
+// both parts' products, bound by the chain from a tile's scores through their
+// softmax and weights to the next scores (4660 cycles a tile of both streams, 3072
+// of them products; 3950 without the second parts' products, 4100 without their
+// stores, so each waits for the other); fp32 with 32 rows 111 us, with 256 rows 265 us
+// (in bf16 parts 1.6 PFLOP/s).
 //
 // Every wait ends: after kWaitNs and a last try of kLastTryNs a thread stops waiting
 // for good and goes on, the rows of the block come out as NaN, and the block ends
