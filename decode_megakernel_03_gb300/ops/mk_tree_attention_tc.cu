@@ -36,11 +36,11 @@
 //
 // Measured, 8 sequences over 16384 keys each, 8B shape (537 MB): bf16 with 64 rows 98
 // us, 5.5 TB/s, bound by the bytes; with 256 rows 168 us, 3.2 TB/s and 1.23 PFLOP/s of
-// both parts' products, bound by the chain from a tile's scores through their
-// softmax and weights to the next scores (4660 cycles a tile of both streams, two
-// thirds of them products, 48 of 64 cycles; 3950 without the second parts' products,
-// 4100 without their stores, so each waits for the other); fp32 with 32 rows 111 us,
-// with 256 rows 265 us (in bf16 parts 1.6 PFLOP/s).
+// both parts' products. Its tiles are bound by the products, with which stores and
+// softmax overlap in part: 4660 cycles or 2.44 us a tile of both streams, 1.57 PFLOP/s
+// at the power limit (a plain library product sustains 1.71); 3950 cycles without
+// the second parts' products, 4100 without their stores. fp32 with 32 rows 111 us, with
+// 256 rows 265 us (in bf16 parts 1.6 PFLOP/s).
 //
 // Every wait ends: after kWaitNs and a last try of kLastTryNs a thread stops waiting
 // for good and goes on, the rows of the block come out as NaN, and the block ends
