@@ -23,8 +23,8 @@ SOURCES = [os.path.join(CSRC, f) for f in (
     "mk_kernel.cu", "mk_kernel_fixed_a.cu", "mk_kernel_fixed_b.cu", "mk_kernel_fx.cu",
     "mk_kernel_dyn.cu", "mk_abi.cu", "mk_sched.cpp", "mk_noalloc.cu")] + [
     os.path.join(OPS, f) for f in (
-        "mk_cache_ops.cu", "mk_tree_attention.cu", "mk_tree_attention_tc.cu", "mk_tree_accept.cu",
-        "mk_pages.cpp")]
+        "mk_cache_ops.cu", "mk_tree_attention.cu", "mk_tree_attention_tc.cu",
+        "mk_prefix_attention.cu", "mk_tree_accept.cu", "mk_tree_verify.cu", "mk_pages.cpp")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
           "-I", CSRC, "-I", OPS]

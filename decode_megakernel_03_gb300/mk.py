@@ -28,8 +28,9 @@ EXPORTS = ("mk_create", "mk_decode_step", "mk_decode_step_multilaunch", "mk_get_
            "mk_debug_permute_queues", "mk_set_dynamic", "mk_schedule_build_dynamic",
            "mk_schedule_build_steps", "mk_prefill",
            # operators over a KV cache
-           "mk_rope_init", "mk_rope_append", "mk_tree_attention", "mk_tree_attention_workspace",
-           "mk_tree_accept", "mk_tree_accept_workspace", "mk_cache_compact",
+           "mk_rope_init", "mk_rope_append", "mk_norm_rope_append", "mk_tree_attention",
+           "mk_tree_attention_workspace", "mk_prefix_attention", "mk_prefix_attention_workspace",
+           "mk_tree_accept", "mk_tree_accept_workspace", "mk_tree_verify", "mk_cache_compact",
            "mk_cache_copy_blocks", "mk_pages_create", "mk_pages_destroy", "mk_pages_resize",
            "mk_pages_fork", "mk_pages_compact", "mk_pages_read")
 
@@ -153,11 +154,18 @@ def lib():
         L.mk_rope_init.argtypes = [ctypes.POINTER(MkRopeConfig), ctypes.POINTER(MkRope)]
         L.mk_rope_append.argtypes = [ctypes.POINTER(MkRope), cachep, i, i, i, i, i, vp, i64, vp,
                                      i64, vp, i64, vp, i64, vp, vp, vp, vp]
+        L.mk_norm_rope_append.argtypes = [ctypes.POINTER(MkRope), vp, vp, ctypes.c_float,
+                                          *L.mk_rope_append.argtypes[1:]]
         L.mk_tree_attention.argtypes = [cachep, i, i, i, i, i, ctypes.c_float, vp, i64, vp, vp, vp,
                                         vp, i64, vp, size, vp]
         L.mk_tree_attention_workspace.argtypes = [cachep, i, i, i, i, sizep]
+        L.mk_prefix_attention.argtypes = [cachep, i, i, i, i, i, ctypes.c_float, vp, i64, i, vp, vp, vp,
+                                          vp, vp, vp, i64, vp, size, vp]
+        L.mk_prefix_attention_workspace.argtypes = [cachep, i, i, i, i, i, sizep]
         L.mk_tree_accept.argtypes = [i, i, i, i, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
         L.mk_tree_accept_workspace.argtypes = [i, i, i, sizep]
+        L.mk_tree_verify.argtypes = [i, i, i, i, vp, i64, i, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp,
+                                     vp, vp, vp]
         L.mk_cache_compact.argtypes = [cachep, i, i, vp, vp, vp, vp]
         L.mk_cache_copy_blocks.argtypes = [cachep, vp, i, vp]
         L.mk_pages_create.argtypes = [i, i, i, i, ctypes.POINTER(vp)]
@@ -606,16 +614,9 @@ def _new(shape, dtype, device, zero: bool):
     return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=device)
 
 
-def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=None, counts=None,
-                q_out=None, stream=None):
-    """mk_rope_append: q [B][T][nh][D], k, v [B][T][nkv][D] (bf16 or fp32; views
-    into a fused projection's rows are fine), starts [B], parents [B][T],
-    counts [B] int32, all on the device. Returns the rotated queries (q_out,
-    which may be q; else a new tensor, whose rows behind counts are 0)."""
+def _rope_args(cache: Cache, q, k, v, starts, parents, counts, q_out):
+    """What the calls of the library share from n_tokens on, up to the stream; q_out."""
     dev = cache.device
-    if (other := _elsewhere(dev, stream)) is not None:
-        with other:
-            return rope_append(rope, cache, layer, q, k, v, starts, parents, counts, q_out)
     shape, kind, qs = _queries(q, cache)
     b, n, nh, d = shape
     kv, dtype = (b, n, cache.n_kv_heads, d), q.dtype
@@ -626,9 +627,46 @@ def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=N
         q_out, os_ = _new(shape, dtype, dev, counts is not None), nh * d
     else:
         os_ = _heads(q_out, shape, dtype, dev, "q_out")
-    _check(lib().mk_rope_append(rope.ref, cache.ref, layer, b, n, nh, kind, q.data_ptr(), qs,
-                                k.data_ptr(), ks, v.data_ptr(), vs, q_out.data_ptr(), os_, sp, pp,
-                                cp, _current_raw(dev.index)))
+    return (b, n, nh, kind, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            q_out.data_ptr(), os_, sp, pp, cp, _current_raw(dev.index)), q_out
+
+
+def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=None, counts=None,
+                q_out=None, stream=None):
+    """mk_rope_append: q [B][T][nh][D], k, v [B][T][nkv][D] (bf16 or fp32; views
+    into a fused projection's rows are fine), starts [B], parents [B][T],
+    counts [B] int32, all on the device. Returns the rotated queries (q_out,
+    which may be q; else a new tensor, whose rows behind counts are 0)."""
+    if (other := _elsewhere(cache.device, stream)) is not None:
+        with other:
+            return rope_append(rope, cache, layer, q, k, v, starts, parents, counts, q_out)
+    args, q_out = _rope_args(cache, q, k, v, starts, parents, counts, q_out)
+    _check(lib().mk_rope_append(rope.ref, cache.ref, layer, *args))
+    return q_out
+
+
+def _norm_weights(t, cache: Cache, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.bfloat16 or t.device != cache.device or not t.is_contiguous():
+        raise _bad(f"{what} must be a contiguous bfloat16 tensor on {cache.device}")
+    if t.shape != (cache.head_dim,):
+        raise _bad(f"{what} has the shape {tuple(t.shape)}, not {(cache.head_dim,)}")
+    return t.data_ptr()
+
+
+def norm_rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, q_norm, k_norm, starts,
+                     parents=None, counts=None, eps: float = 1e-6, q_out=None, stream=None):
+    """mk_norm_rope_append: rope_append of queries and keys whose heads are first
+    divided by their root mean square and multiplied by q_norm, k_norm (bf16 [D]
+    on the device; None: ones)."""
+    if (other := _elsewhere(cache.device, stream)) is not None:
+        with other:
+            return norm_rope_append(rope, cache, layer, q, k, v, q_norm, k_norm, starts, parents,
+                                    counts, eps, q_out)
+    qn, kn = _norm_weights(q_norm, cache, "q_norm"), _norm_weights(k_norm, cache, "k_norm")
+    args, q_out = _rope_args(cache, q, k, v, starts, parents, counts, q_out)
+    _check(lib().mk_norm_rope_append(rope.ref, qn, kn, eps, cache.ref, layer, *args))
     return q_out
 
 
@@ -663,6 +701,50 @@ def tree_attention(cache: Cache, layer: int, q, starts, parents=None, counts=Non
     return out
 
 
+def prefix_attention(cache: Cache, layer: int, q, first, prefix, starts, parents=None, counts=None,
+                     scale=None, out=None, stream=None):
+    """mk_prefix_attention: tree_attention of a batch whose groups share a prefix.
+    first, prefix [n_groups] int32 on the device: each group's first sequence, and how
+    many of its slots the group shares (the first sequence's rows are read)."""
+    dev = cache.device
+    if (other := _elsewhere(dev, stream)) is not None:
+        with other:
+            return prefix_attention(cache, layer, q, first, prefix, starts, parents, counts, scale, out)
+    shape, kind, qs = _queries(q, cache)
+    b, n, nh, d = shape
+    if len(first.shape) != 1:
+        raise _bad("first must be [groups]")
+    groups = first.shape[0]
+    fp, xp = _ints(first, dev, "first", (groups,)), _ints(prefix, dev, "prefix", (groups,))
+    sp = _ints(starts, dev, "starts", (b,))
+    pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
+    size = cache.workspaces.get((b, n, nh, kind, groups))
+    if size is None:
+        need = ctypes.c_size_t()
+        _check(lib().mk_prefix_attention_workspace(cache.ref, b, n, nh, kind, groups,
+                                                   ctypes.byref(need)))
+        size = cache.workspaces[b, n, nh, kind, groups] = need.value
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    if out is None:
+        out, os_ = _new(shape, q.dtype, dev, counts is not None), nh * d
+    else:
+        os_ = _heads(out, shape, q.dtype, dev, "out")
+    _check(lib().mk_prefix_attention(cache.ref, layer, b, n, nh, kind,
+                                     d ** -0.5 if scale is None else scale, q.data_ptr(), qs, groups,
+                                     fp, xp, sp, pp, cp, out.data_ptr(), os_, ws.data_ptr(), size,
+                                     _current_raw(dev.index)))
+    return out
+
+
+def _rows(t, shape, what: str) -> int:
+    """The row stride of t [B][T][V]: rows packed and evenly spaced."""
+    b, n, vocab = shape
+    sb, sn, sv = t.stride()
+    if (vocab > 1 and sv != 1) or (n > 1 and b > 1 and sb != n * sn):
+        raise _bad(f"{what}: rows must be packed and evenly spaced")
+    return (sb if b > 1 else vocab) if n == 1 else sn
+
+
 def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     """mk_tree_accept: logits [B][T][V] (bf16 or fp32), tokens [B][T] int32.
     Returns int32 (choices [B][T], path [B][T], accepted [B], next [B])."""
@@ -675,10 +757,7 @@ def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
             return tree_accept(logits, tokens, parents, counts)
     kind = _type_of(logits, "logits")
     b, n, vocab = shape
-    sb, sn, sv = logits.stride()
-    stride = (sb if b > 1 else vocab) if n == 1 else sn
-    if (vocab > 1 and sv != 1) or (n > 1 and b > 1 and sb != n * sn):
-        raise _bad("logits: rows must be packed and evenly spaced")
+    stride = _rows(logits, shape, "logits")
     tp = _ints(tokens, dev, "tokens", (b, n))
     pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
     need = ctypes.c_size_t()
@@ -694,6 +773,58 @@ def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     last = first + 2 * rows
     return (buf.as_strided((b, n), (n, 1), first), buf.as_strided((b, n), (n, 1), first + rows),
             buf.as_strided((b,), (1,), last), buf.as_strided((b,), (1,), last + b))
+
+
+def _floats(t, device, what: str, shape):
+    """The pointer of an fp32 tensor (contiguous, on `device`)."""
+    if t is None:
+        return None
+    if (getattr(t, "dtype", None) != torch.float32 or t.device != device
+            or not t.is_contiguous()):
+        raise _bad(f"{what} must be a contiguous float32 tensor on {device}")
+    if t.shape != shape:
+        raise _bad(f"{what} has the shape {tuple(t.shape)}, not {shape}")
+    return t.data_ptr()
+
+
+def tree_verify(logits, tokens, uniform, noise, parents=None, counts=None, draft=None,
+                temperature=None, stream=None):
+    """mk_tree_verify: logits [B][T][V] (bf16 or fp32), tokens [B][T] int32,
+    uniform [B][T] fp32 in [0, 1), noise [B][V] fp32 (exponential, mean 1; its rows
+    packed); draft [B][T][V] (bf16 or fp32) the distributions that each node's children
+    were sampled from, or None; temperature [B] fp32. Returns int32 (path [B][T],
+    accepted [B], next [B])."""
+    _use_torch()
+    dev, shape = logits.device, logits.shape
+    if not logits.is_cuda or len(shape) != 3:
+        raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
+    if (other := _elsewhere(dev, stream)) is not None:
+        with other:
+            return tree_verify(logits, tokens, uniform, noise, parents, counts, draft, temperature)
+    kind = _type_of(logits, "logits")
+    b, n, vocab = shape
+    stride = _rows(logits, shape, "logits")
+    draft_kind, draft_at, draft_stride = 0, None, 0
+    if draft is not None:
+        if draft.device != dev or draft.shape != shape:
+            raise _bad(f"draft must be a tensor of the shape {tuple(shape)} on {dev}")
+        draft_kind, draft_stride = _type_of(draft, "draft"), _rows(draft, shape, "draft")
+        draft_at = draft.data_ptr()
+    if noise.dtype != torch.float32 or noise.device != dev or noise.shape != (b, vocab) or (
+            vocab > 1 and noise.stride(1) != 1):
+        raise _bad(f"noise must be a float32 tensor of the shape {(b, vocab)} on {dev}, its rows packed")
+    tp, up = _ints(tokens, dev, "tokens", (b, n)), _floats(uniform, dev, "uniform", (b, n))
+    pp, cp = _ints(parents, dev, "parents", (b, n)), _ints(counts, dev, "counts", (b,))
+    hp = _floats(temperature, dev, "temperature", (b,))
+    rows = b * n
+    buf = torch.empty(rows + 2 * b, dtype=torch.int32, device=dev)
+    at = buf.data_ptr()
+    _check(lib().mk_tree_verify(b, n, vocab, kind, logits.data_ptr(), stride, draft_kind, draft_at,
+                                draft_stride, hp, tp, pp, cp, up, noise.data_ptr(),
+                                noise.stride(0) if b > 1 else vocab, at, at + 4 * rows,
+                                at + 4 * rows + 4 * b, _current_raw(dev.index)))
+    return (buf.as_strided((b, n), (n, 1), 0), buf.as_strided((b,), (1,), rows),
+            buf.as_strided((b,), (1,), rows + b))
 
 
 def cache_compact(cache: Cache, starts, path, accepted, stream=None):

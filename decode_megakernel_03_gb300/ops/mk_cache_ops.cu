@@ -126,6 +126,9 @@ struct RopeParams {
   int64_t qs, ks, vs, os;  // row strides in elements
   const int32_t *starts, *parents, *counts;
   int rows, T, nh, tokens;  // rows = batch * T; tokens per block
+  // mk_norm_rope_append: the weights (nullptr: ones) and what is added to a mean square
+  const uint16_t *q_norm, *k_norm;
+  float eps;
 };
 
 // A block takes `tokens` rows: one angle per (token, pair), shared by all heads
@@ -143,7 +146,11 @@ struct RopeParams {
 // Bound by the bytes of the rows: 32768 rows of the 8B shape, bf16, 805 MB, take
 // 125 us as neighbours, 6.4 TB/s; U heads of a lane are in flight: 133 us with 2,
 // 136 with 8. 200 rows take 4 to 5 us, a launch's latency.
-template <typename T, int D, int PIECE>
+// NORM: a head of q or k is first divided by its root mean square and multiplied by
+// its weights, x w / sqrt(sum x^2 / D + eps). The sum of squares is fp32, over the
+// lane's eight elements and then over the head's lanes by shuffles; one that leaves
+// fp32's range is taken again from x 2^-70. The rounded value is the rotated one only.
+template <typename T, int D, int PIECE, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
   __shared__ float2 cs[kRopeTokens][D / 2];
@@ -223,6 +230,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     turns[j] = 4 * c + j < half;
     w[j] = cs[tok][4 * c + j];
   }
+  uint32_t weight[2][4];  // of q and k, bf16 pairs, NORM only
+  if constexpr (NORM) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) weight[i / 4][i % 4] = 0x3f803f80u;  // ones
+    if (p.q_norm) {
+#pragma unroll
+      for (int i = 0; i < 8 / N; ++i) load<N>(p.q_norm + at[i], weight[0], N * i);
+    }
+    if (p.k_norm) {
+#pragma unroll
+      for (int i = 0; i < 8 / N; ++i) load<N>(p.k_norm + at[i], weight[1], N * i);
+    }
+  }
   for (int base = warp / p.tokens * HPW; base < heads; base += U * step) {
     uint32_t x[U][2 * sizeof(T)];
 #pragma unroll
@@ -244,6 +264,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = elem<T>(x[u], j);
       if (head < p.nh + n_kv) {
+        if constexpr (NORM) {
+          const unsigned mine = (LPH == 8 ? 0xffu : 0xffffu) << (lane / LPH * LPH);  // the head's lanes
+          auto squares = [&] {
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s = fmaf(o[j], o[j], s);
+#pragma unroll
+            for (int d = 1; d < LPH; d *= 2) s += __shfl_xor_sync(mine, s, d);
+            return s * (1.f / D);
+          };
+          float mean = squares(), eps = p.eps;
+          if (!(mean < INFINITY)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] *= 0x1p-70f;
+            mean = squares();
+            eps = 0.f;  // below a rounding of a mean of 2^121 and more
+          }
+          const float f = __frsqrt_rn(mean + eps);
+          const uint32_t* by = head < p.nh ? weight[0] : weight[1];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] *= f * elem<uint16_t>(by, j);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = N == 8 ? 2 * j : j, k = N == 8 ? 2 * j + 1 : j + 4;
@@ -269,14 +311,71 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool NORM>
 void launch_rope(const RopeParams& p, cudaStream_t st) {
   const dim3 grid((p.rows + p.tokens - 1) / p.tokens);
   const int half = p.rope.rotary_dim / 2;
-  if (p.rope.interleaved) rope_append_kernel<T, D, 8><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (half % 4 == 0) rope_append_kernel<T, D, 4><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (half % 2 == 0) rope_append_kernel<T, D, 2><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_append_kernel<T, D, 1><<<grid, kRopeThreads, 0, st>>>(p);
+  if (p.rope.interleaved) rope_append_kernel<T, D, 8, NORM><<<grid, kRopeThreads, 0, st>>>(p);
+  else if (half % 4 == 0) rope_append_kernel<T, D, 4, NORM><<<grid, kRopeThreads, 0, st>>>(p);
+  else if (half % 2 == 0) rope_append_kernel<T, D, 2, NORM><<<grid, kRopeThreads, 0, st>>>(p);
+  else rope_append_kernel<T, D, 1, NORM><<<grid, kRopeThreads, 0, st>>>(p);
+}
+
+// mk_rope_append and, with NORM, mk_norm_rope_append: the checks that they share, and
+// the launch. p holds the weights and eps already.
+template <bool NORM>
+int rope_append(RopeParams& p, const char* name, const mk_rope* rope, const mk_cache* cache,
+                int layer, int batch, int n_tokens, int n_heads, int type, const void* q,
+                int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                void* q_out, int64_t q_out_stride, const int32_t* starts, const int32_t* parents,
+                const int32_t* counts, void* stream) {
+  if (int rc = check_cache(cache, batch, true, &p.cache)) return rc;
+  if (!rope || !q || !k || !v || !q_out || !starts)
+    return op_fail(MK_ERR_INVALID, NORM ? "mk_norm_rope_append: a NULL argument"
+                                        : "mk_rope_append: a NULL argument");
+
+  if (layer < 0 || layer >= cache->n_layers)
+    return op_fail(MK_ERR_INVALID, "layer out of range [0, n_layers)");
+  if (type != MK_TYPE_BF16 && type != MK_TYPE_FP32)
+    return op_fail(MK_ERR_INVALID, "type must be MK_TYPE_BF16 or MK_TYPE_FP32");
+  if (rope->head_dim != cache->head_dim || rope->rotary_dim < 2 ||
+      rope->rotary_dim > rope->head_dim || rope->rotary_dim % 2)
+    return op_fail(MK_ERR_INVALID, "rope is not a plan for this head_dim");
+  if (n_tokens < 1 || (int64_t)batch * n_tokens > (1 << 30))
+    return op_fail(MK_ERR_INVALID, "n_tokens must be at least 1 and batch x n_tokens at most 2^30");
+  if (parents && n_tokens > MK_MAX_TREE)
+    return op_fail(MK_ERR_INVALID, "a tree has at most MK_MAX_TREE nodes");
+  if (n_heads < 1 || n_heads > 4096 || cache->n_kv_heads > 4096)
+    return op_fail(MK_ERR_INVALID, "n_heads and n_kv_heads must be 1 to 4096");
+  const int unit = type == MK_TYPE_FP32 ? 4 : 8;
+  const int64_t need[4] = {n_heads, cache->n_kv_heads, cache->n_kv_heads, n_heads};
+  const int64_t have[4] = {q_stride, k_stride, v_stride, q_out_stride};
+  const void* at[4] = {q, k, v, q_out};
+  for (int i = 0; i < 4; ++i)
+    if (!aligned(at[i], 16) || have[i] % unit || have[i] < need[i] * cache->head_dim)
+      return op_fail(MK_ERR_INVALID,
+                     "q, k, v, q_out: 16-byte aligned rows, strides at least a row, are needed");
+  p.rope = *rope;
+  p.k_cache = (uint16_t*)cache->k[layer];
+  p.v_cache = (uint16_t*)cache->v[layer];
+  p.q = q, p.k = k, p.v = v, p.q_out = q_out;
+  p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.os = q_out_stride;
+  p.starts = starts, p.parents = parents, p.counts = counts;
+  p.rows = batch * n_tokens, p.T = n_tokens, p.nh = n_heads;
+  // Rows of a block: one where the blocks are few (8B shape, bf16, 512 rows: 6.2 us
+  // against 7.2 with four), four where there are enough, since a block's rows
+  // then find their angles together (1024 rows 7.2 us against 8.2 with one, 2048
+  // 11.0 against 14.1, 32768 126 against 168).
+  p.tokens = p.rows >= 1024 ? kRopeTokens : 1;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (type == MK_TYPE_FP32) {
+    if (cache->head_dim == 64) launch_rope<float, 64, NORM>(p, st);
+    else launch_rope<float, 128, NORM>(p, st);
+  } else {
+    if (cache->head_dim == 64) launch_rope<uint16_t, 64, NORM>(p, st);
+    else launch_rope<uint16_t, 128, NORM>(p, st);
+  }
+  return op_cuda(cudaGetLastError(), name);
 }
 
 // ---- accepted rows moved down ------------------------------------------------------
@@ -485,51 +584,30 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
                    int64_t q_out_stride, const int32_t* starts, const int32_t* parents,
                    const int32_t* counts, void* stream) {
   RopeParams p;
-  if (int rc = check_cache(cache, batch, true, &p.cache)) return rc;
-  if (!rope || !q || !k || !v || !q_out || !starts)
-    return op_fail(MK_ERR_INVALID, "mk_rope_append: a NULL argument");
-  if (layer < 0 || layer >= cache->n_layers)
-    return op_fail(MK_ERR_INVALID, "layer out of range [0, n_layers)");
-  if (type != MK_TYPE_BF16 && type != MK_TYPE_FP32)
-    return op_fail(MK_ERR_INVALID, "type must be MK_TYPE_BF16 or MK_TYPE_FP32");
-  if (rope->head_dim != cache->head_dim || rope->rotary_dim < 2 ||
-      rope->rotary_dim > rope->head_dim || rope->rotary_dim % 2)
-    return op_fail(MK_ERR_INVALID, "rope is not a plan for this head_dim");
-  if (n_tokens < 1 || (int64_t)batch * n_tokens > (1 << 30))
-    return op_fail(MK_ERR_INVALID, "n_tokens must be at least 1 and batch x n_tokens at most 2^30");
-  if (parents && n_tokens > MK_MAX_TREE)
-    return op_fail(MK_ERR_INVALID, "a tree has at most MK_MAX_TREE nodes");
-  if (n_heads < 1 || n_heads > 4096 || cache->n_kv_heads > 4096)
-    return op_fail(MK_ERR_INVALID, "n_heads and n_kv_heads must be 1 to 4096");
-  const int unit = type == MK_TYPE_FP32 ? 4 : 8;
-  const int64_t need[4] = {n_heads, cache->n_kv_heads, cache->n_kv_heads, n_heads};
-  const int64_t have[4] = {q_stride, k_stride, v_stride, q_out_stride};
-  const void* at[4] = {q, k, v, q_out};
-  for (int i = 0; i < 4; ++i)
-    if (!aligned(at[i], 16) || have[i] % unit || have[i] < need[i] * cache->head_dim)
-      return op_fail(MK_ERR_INVALID,
-                     "q, k, v, q_out: 16-byte aligned rows, strides at least a row, are needed");
-  p.rope = *rope;
-  p.k_cache = (uint16_t*)cache->k[layer];
-  p.v_cache = (uint16_t*)cache->v[layer];
-  p.q = q, p.k = k, p.v = v, p.q_out = q_out;
-  p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.os = q_out_stride;
-  p.starts = starts, p.parents = parents, p.counts = counts;
-  p.rows = batch * n_tokens, p.T = n_tokens, p.nh = n_heads;
-  // Rows of a block: one where the blocks are few (8B shape, bf16, 512 rows: 6.2 us
-  // against 7.2 with four), four where there are enough, since a block's rows
-  // then find their angles together (1024 rows 7.2 us against 8.2 with one, 2048
-  // 11.0 against 14.1, 32768 126 against 168).
-  p.tokens = p.rows >= 1024 ? kRopeTokens : 1;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (type == MK_TYPE_FP32) {
-    if (cache->head_dim == 64) launch_rope<float, 64>(p, st);
-    else launch_rope<float, 128>(p, st);
-  } else {
-    if (cache->head_dim == 64) launch_rope<uint16_t, 64>(p, st);
-    else launch_rope<uint16_t, 128>(p, st);
-  }
-  return op_cuda(cudaGetLastError(), "mk_rope_append");
+  p.q_norm = p.k_norm = nullptr;
+  p.eps = 0.f;
+  return rope_append<false>(p, "mk_rope_append", rope, cache, layer, batch, n_tokens, n_heads, type, q,
+                            q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, starts, parents,
+                            counts, stream);
+}
+
+int mk_norm_rope_append(const mk_rope* rope, const void* q_norm, const void* k_norm, float eps,
+                        const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
+                        int type, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                        const int32_t* starts, const int32_t* parents, const int32_t* counts,
+                        void* stream) {
+  if (!aligned(q_norm, 16) || !aligned(k_norm, 16))
+    return op_fail(MK_ERR_INVALID, "q_norm, k_norm: not 16-byte aligned");
+  if (!(eps >= 1e-30f) || !(eps <= 1.f))
+    return op_fail(MK_ERR_INVALID, "eps must be 1e-30 to 1");
+  RopeParams p;
+  p.q_norm = (const uint16_t*)q_norm;
+  p.k_norm = (const uint16_t*)k_norm;
+  p.eps = eps;
+  return rope_append<true>(p, "mk_norm_rope_append", rope, cache, layer, batch, n_tokens, n_heads, type, q,
+                            q_stride, k, k_stride, v, v_stride, q_out, q_out_stride, starts, parents,
+                            counts, stream);
 }
 
 int mk_cache_compact(const mk_cache* cache, int batch, int n_tokens, const int32_t* starts,

@@ -644,7 +644,7 @@ int launch(const AttnParams& p, cudaStream_t st) {
   using Lay = Layout<D, P>;
   auto* fn = tree_attention_kernel<D, P>;
   static std::atomic<uint64_t> ready{0};
-  if (int rc = allow_shared(ready, (const void*)fn, Lay::kBytes)) return rc;
+  if (int rc = allow_shared(ready, (const void*)fn, Lay::kBytes, "mk_tree_attention")) return rc;
   fn<<<p.groups * p.row_tiles, kThreads, Lay::kBytes, st>>>(p);
   return op_cuda(cudaGetLastError(), "mk_tree_attention");
 }

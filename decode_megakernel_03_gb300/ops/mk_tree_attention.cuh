@@ -22,7 +22,12 @@
 
 namespace mk {
 
+struct Line;
+struct Share;
+
 struct AttnParams {
+  using Line = mk::Line;
+  using Share = mk::Share;
   CacheView cache;
   const uint16_t *k, *v;
   const void* q;
@@ -86,12 +91,17 @@ __device__ __forceinline__ void work_line(const AttnParams& p, Line& line) {
   __syncwarp();
 }
 
+__device__ __forceinline__ int all_places(const AttnParams& p, const Line& line) {
+  return line.prefix[p.B];
+}
+
 // The cut of a line of W places: group s has the places [begin(s), begin(s + 1)),
 // begin(s) = floor(s W / groups) = s q + floor(s r / groups).
 struct Cut {
   int W, groups, q, r;
   uint32_t inv;
-  __device__ __forceinline__ Cut(int W_, const AttnParams& p)
+  template <class P>
+  __device__ __forceinline__ Cut(int W_, const P& p)
       : W(W_), groups(p.groups), inv(p.inv_groups) {
     q = (int)__umulhi((uint32_t)W, inv);  // at most one off, as W < 2^31
     r = W - q * groups;
@@ -161,6 +171,27 @@ __device__ __forceinline__ int64_t row_offset(const AttnParams& p, int b, int g,
   return ((int64_t)b * p.T + row / p.G) * stride + (g * p.G + row % p.G) * D;
 }
 
+// What the kernel for many rows asks about a share: the slot of its first key, its
+// first row, whether a row is there, the node that a row belongs to, whether the share
+// is all that the row sees (its output is written then, else its sums to share_slot).
+__device__ __forceinline__ int first_slot(const Share&) { return 0; }
+__device__ __forceinline__ int first_row(const Share&) { return 0; }
+__device__ __forceinline__ bool row_there(const AttnParams&, const Line&, const Share& sh, int row) {
+  return row < sh.rows;
+}
+__device__ __forceinline__ int row_node(const AttnParams& p, const Share&, int row) {
+  return row / p.G;
+}
+__device__ __forceinline__ int64_t row_offset(const AttnParams& p, const Share& sh, int row, int D,
+                                              int64_t stride) {
+  return row_offset(p, sh.b, sh.g, row, D, stride);
+}
+__device__ __forceinline__ bool is_final(const Share& sh) { return sh.n == sh.nt; }
+__device__ __forceinline__ size_t share_slot(const AttnParams& p, int group, const Share& sh, int rt,
+                                             int local, int) {
+  return part_slot(p, group, sh.begins, rt) * p.row_tile + local;
+}
+
 // ---- asynchronous 16-byte copies ---------------------------------------------------
 // (bytes 0: the destination is zeroed)
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -195,14 +226,14 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[P]) {
 
 // Allows a kernel its dynamic shared memory, once on each device (ready: a bit per
 // device; doing it twice does no harm).
-inline int allow_shared(std::atomic<uint64_t>& ready, const void* fn, int bytes) {
+inline int allow_shared(std::atomic<uint64_t>& ready, const void* fn, int bytes, const char* name) {
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  if (e != cudaSuccess) return op_cuda(e, name);
   const uint64_t bit = 1ull << (device & 63);
   if (device < 64 && (ready.load(std::memory_order_acquire) & bit)) return MK_OK;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
+  if (e != cudaSuccess) return op_cuda(e, name);
   ready.fetch_or(bit, std::memory_order_release);
   return MK_OK;
 }

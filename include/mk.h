@@ -432,6 +432,20 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
                    int64_t q_out_stride, const int32_t* starts, const int32_t* parents,
                    const int32_t* counts, void* stream);
 
+/* mk_rope_append for a model that normalises each head of its queries and keys
+   before their rotation: a head x becomes x w / sqrt(mean of x^2 + eps), in fp32,
+   in the same pass; what is rounded is the rotated value only. q_norm, k_norm:
+   DEVICE bf16 [head_dim], 16-byte aligned, shared by the heads; NULL: ones. eps
+   1e-30 to 1. Values pass as they are. A NaN or an infinity in a head of q or k stays with that
+   head. The other arguments and the errors are those of mk_rope_append.
+   (mk_decode_step and the other calls with a handle do not normalise heads.) */
+int mk_norm_rope_append(const mk_rope* rope, const void* q_norm, const void* k_norm, float eps,
+                        const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
+                        int type, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, void* q_out, int64_t q_out_stride,
+                        const int32_t* starts, const int32_t* parents, const int32_t* counts,
+                        void* stream);
+
 /* Attention of the tree's nodes over layer `layer` of the cache: node t sees
    the slots below starts[b], its ancestors' and its own (their rows are in the
    cache already: mk_rope_append). q, out: DEVICE `type`, rows as above
@@ -457,6 +471,28 @@ int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens,
 int mk_tree_attention_workspace(const mk_cache* cache, int batch, int n_tokens, int n_heads,
                                 int type, size_t* bytes);
 
+/* mk_tree_attention for a batch whose groups share a prefix (the samples of a prompt,
+   mk_pages_fork): the prefix's keys are read once for all sequences of a group.
+   first, prefix: DEVICE int32 [n_groups], n_groups 1 to batch. Group i is the
+   sequences from first[i] on, up to the next group's first (the last: to the
+   batch's end); a first below the one before it or outside [0, batch] is taken at the nearest bound, a group
+   may come out empty, and sequences before first[0] share nothing. The slots
+   below prefix[i] (at least 0, at most the smallest starts of the group's sequences that have
+   nodes) hold the same rows for the whole group: those of the group's FIRST sequence are
+   read, the others' table entries for whole pages of them are not. Everything else is
+   as in mk_tree_attention, whose result this is where the group's tables agree,
+   up to the order of its sums.
+   Errors: MK_ERR_INVALID (also a workspace below the query's size), MK_ERR_CUDA. */
+int mk_prefix_attention(const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
+                        int type, float scale, const void* q, int64_t q_stride, int n_groups,
+                        const int32_t* first, const int32_t* prefix, const int32_t* starts,
+                        const int32_t* parents, const int32_t* counts, void* out,
+                        int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace that mk_prefix_attention needs for these arguments on the
+   current device (*bytes). */
+int mk_prefix_attention_workspace(const mk_cache* cache, int batch, int n_tokens, int n_heads,
+                                  int type, int n_groups, size_t* bytes);
+
 /* Greedy acceptance of a drafted tree. Node 0 is each sequence's last token;
    logits (DEVICE `type`, row b * n_tokens + t of `vocab` values at a stride of
    logits_stride elements) are those after each node, tokens (DEVICE int32
@@ -473,6 +509,36 @@ int mk_tree_accept(int batch, int n_tokens, int vocab, int type, const void* log
                    const int32_t* counts, int32_t* choices, int32_t* path, int32_t* accepted,
                    int32_t* next, void* workspace, size_t workspace_bytes, void* stream);
 int mk_tree_accept_workspace(int batch, int n_tokens, int vocab, size_t* bytes);
+
+/* Verification of a drafted tree by rejection sampling: what is accepted, and the
+   token after it, are distributed as if they had been sampled from the target one
+   by one. The arguments of mk_tree_accept, and:
+   temperature (DEVICE fp32 [batch], NULL: 1): a row's probabilities p are the
+   softmax of its logits / temperature; at one that is not above 0, NaN included, the
+   first largest logit has them all. A logit that is NaN or -inf has probability 0.
+   draft (DEVICE `draft_type`, rows as the logits', at draft_stride): row t is the
+   distribution q that the children of node t were each sampled from (values below 0 and
+   NaN count as 0); NULL: the children were proposed without one. uniform (DEVICE fp32 [batch][n_tokens]), the
+   number in [0, 1) by which each node is accepted or not (node 0's is not used; others are taken at the
+   nearer bound, NaN as 0); noise (DEVICE fp32, row b at b * noise_stride): `vocab` numbers of an exponential
+   distribution with mean 1 (taken at 1e-30 below it and NaN, at 1e30 above it).
+   From node 0 on, the children of a node are taken in ascending order: child t
+   with token x is accepted if uniform[t] q(x) < r(x), where r is p at first; the
+   walk goes on from it. After a rejection r becomes max(r - q, 0), scaled to sum
+   1 (without draft: r without x, scaled; q(x) is 1 above). Where no child is
+   accepted, next is the index of the largest r / noise (the lowest among equal
+   ones), a sample of r. A token outside [0, vocab) is passed over, and what hangs
+   off it with it. Where rounding leaves nothing of r, next is sampled from p. In a row
+   without a logit above -inf there is no p: nothing is accepted, next is -1. Probabilities and sums
+   are fp32 (2^-20 of their value, differences 2^-20 of what is subtracted): a comparison closer than
+   that may fall either way, the same way each time. Outputs as mk_tree_accept's (path, accepted, next).
+   Errors: MK_ERR_INVALID, MK_ERR_CUDA. */
+int mk_tree_verify(int batch, int n_tokens, int vocab, int type, const void* logits,
+                   int64_t logits_stride, int draft_type, const void* draft, int64_t draft_stride,
+                   const float* temperature, const int32_t* tokens, const int32_t* parents,
+                   const int32_t* counts, const float* uniform, const float* noise,
+                   int64_t noise_stride, int32_t* path, int32_t* accepted, int32_t* next,
+                   void* stream);
 
 /* Moves the accepted rows down behind the context, in every layer, K and V:
    row starts[b] + i <- row starts[b] + path[b][i] for i < accepted[b] (DEVICE
