@@ -131,31 +131,15 @@ struct RopeParams {
   float eps;
 };
 
-// A block takes `tokens` rows: one angle per (token, pair), shared by all heads
-// (sincospif of a fraction of a turn found by a 64-bit fixed-point product: position
-// times the plan's own 2^-53 turns off, less than fp32's rounding up to position 2^27).
-// Then a warp takes heads of q, k and v of one row, D / 8 lanes to a head. A lane
-// has four pairs, both members of each, so that its sines and cosines stay in its
-// registers and nothing is exchanged (q_out may be q). PIECE: elements that lie
-// together for a lane, 8 when the pairs are neighbours, else the largest of 4, 2, 1
-// that divides rotary_dim / 2; the elements behind rotary_dim are taken as
-// neighbours.
-// (Eight elements in a row per lane and the partners by shuffles: 218 us
-// against 132 for the 32768 rows below in halves of 64, 450 against 138 in
-// halves of 62, where the partners were loaded one by one.)
-// Bound by the bytes of the rows: 32768 rows of the 8B shape, bf16, 805 MB, take
-// 125 us as neighbours, 6.4 TB/s; U heads of a lane are in flight: 133 us with 2,
-// 136 with 8. 200 rows take 4 to 5 us, a launch's latency.
-// NORM: a head of q or k is first divided by its root mean square and multiplied by
-// its weights, x w / sqrt(sum x^2 / D + eps). The sum of squares is fp32, over the
-// lane's eight elements and then over the head's lanes by shuffles; one that leaves
-// fp32's range is taken again from x 2^-70. The rounded value is the rotated one only.
-template <typename T, int D, int PIECE, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
-  __shared__ float2 cs[kRopeTokens][D / 2];
-  __shared__ int s_pos[kRopeTokens];
-  __shared__ uint32_t s_row[kRopeTokens];
+// The block's rows: each token's position (-1: the row is not there), cache row and angles.
+template <int D>
+struct RopeRows {
+  float2 cs[kRopeTokens][D / 2];
+  int pos[kRopeTokens];
+  uint32_t row[kRopeTokens];
+};
+template <int D>
+__device__ __forceinline__ void find_rows(const RopeParams& p, RopeRows<D>& s) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int row0 = blockIdx.x * p.tokens;
   if (warp < p.tokens) {
@@ -185,8 +169,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
       }
     }
     if (lane == 0) {
-      s_pos[warp] = pos;
-      s_row[warp] = crow;
+      s.pos[warp] = pos;
+      s.row[warp] = crow;
     }
   }
   __syncthreads();
@@ -194,21 +178,45 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
     const int tok = i / (D / 2), pair = i % (D / 2);
     float2 v = make_float2(1.f, 0.f);  // behind rotary_dim: passes through
     if (2 * pair < p.rope.rotary_dim) {
-      const int64_t turn = (int64_t)(p.rope.turns[pair] * (uint64_t)max(s_pos[tok], 0));
+      const int64_t turn = (int64_t)(p.rope.turns[pair] * (uint64_t)max(s.pos[tok], 0));
       sincospif(2.f * ((float)turn * 0x1p-64f), &v.y, &v.x);
       v.x *= p.rope.magnitude;
       v.y *= p.rope.magnitude;
     }
-    cs[tok][pair] = v;
+    s.cs[tok][pair] = v;
   }
   __syncthreads();
+}
+
+// A block takes `tokens` rows: one angle per (token, pair), shared by all heads
+// (sincospif of a fraction of a turn found by a 64-bit fixed-point product: position
+// times the plan's own 2^-53 turns off, less than fp32's rounding up to position 2^27).
+// Then a warp takes heads of q, k and v of one row, D / 8 lanes to a head. A lane
+// has four pairs, both members of each, so that its sines and cosines stay in its
+// registers and nothing is exchanged (q_out may be q). PIECE: elements that lie
+// together for a lane, 8 when the pairs are neighbours, else the largest of 4, 2, 1
+// that divides rotary_dim / 2; the elements behind rotary_dim are taken as
+// neighbours.
+// (Eight elements in a row per lane and the partners by shuffles: 218 us
+// against 132 for the 32768 rows below in halves of 64, 450 against 138 in
+// halves of 62, where the partners were loaded one by one.)
+// Bound by the bytes of the rows: 32768 rows of the 8B shape, bf16, 805 MB, take
+// 125 us as neighbours, 6.4 TB/s; U heads of a lane are in flight: 133 us with 2,
+// 136 with 8. 200 rows take 4 to 5 us, a launch's latency.
+template <typename T, int D, int PIECE>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
+  __shared__ RopeRows<D> s;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int row0 = blockIdx.x * p.tokens;
+  find_rows<D>(p, s);
 
   const int tok = warp % p.tokens;  // tokens divides WARPS
-  if (s_pos[tok] < 0) return;
+  if (s.pos[tok] < 0) return;
   const int n_kv = p.cache.n_kv, heads = p.nh + 2 * n_kv, step = WARPS / p.tokens * HPW;
   const int c = lane % LPH, half = p.rope.rotary_dim / 2;
   const int64_t row = row0 + tok;
-  const uint32_t crow = s_row[tok];
+  const uint32_t crow = s.row[tok];
   // piece i of the lane (elements N i to N i + N - 1 of its eight) starts at `at`;
   // elements j and j + 4 (neighbours: 2j and 2j + 1) are its pair j
   constexpr int N = PIECE, FIRST = N == 8 ? 1 : 4 / N;
@@ -228,20 +236,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     turns[j] = 4 * c + j < half;
-    w[j] = cs[tok][4 * c + j];
-  }
-  uint32_t weight[2][4];  // of q and k, bf16 pairs, NORM only
-  if constexpr (NORM) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) weight[i / 4][i % 4] = 0x3f803f80u;  // ones
-    if (p.q_norm) {
-#pragma unroll
-      for (int i = 0; i < 8 / N; ++i) load<N>(p.q_norm + at[i], weight[0], N * i);
-    }
-    if (p.k_norm) {
-#pragma unroll
-      for (int i = 0; i < 8 / N; ++i) load<N>(p.k_norm + at[i], weight[1], N * i);
-    }
+    w[j] = s.cs[tok][4 * c + j];
   }
   for (int base = warp / p.tokens * HPW; base < heads; base += U * step) {
     uint32_t x[U][2 * sizeof(T)];
@@ -264,28 +259,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = elem<T>(x[u], j);
       if (head < p.nh + n_kv) {
-        if constexpr (NORM) {
-          const unsigned mine = (LPH == 8 ? 0xffu : 0xffffu) << (lane / LPH * LPH);  // the head's lanes
-          auto squares = [&] {
-            float s = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(o[j], o[j], s);
-#pragma unroll
-            for (int d = 1; d < LPH; d *= 2) s += __shfl_xor_sync(mine, s, d);
-            return s * (1.f / D);
-          };
-          float mean = squares(), eps = p.eps;
-          if (!(mean < INFINITY)) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] *= 0x1p-70f;
-            mean = squares();
-            eps = 0.f;  // below a rounding of a mean of 2^121 and more
-          }
-          const float f = __frsqrt_rn(mean + eps);
-          const uint32_t* by = head < p.nh ? weight[0] : weight[1];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] *= f * elem<uint16_t>(by, j);
-        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = N == 8 ? 2 * j : j, k = N == 8 ? 2 * j + 1 : j + 4;
@@ -311,14 +284,163 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
   }
 }
 
-template <typename T, int D, bool NORM>
+// The same of heads that are normalised first: a head x of q or k becomes x w f,
+// f = 1 / sqrt(sum x^2 / D + eps), and then turns. What does not depend on the head is
+// put together once for a row: a pair (a, b) with weights (v, w) becomes
+//   f (a v cos - b w sin), f (a v sin + b w cos),
+// four products of a weight and an angle that stay in a lane's registers while it goes
+// through its heads (of q, then of k and v), pair by pair in two-wide arithmetic: with the
+// weights and the rotation one after another the instructions, not the bytes, took the
+// time (170 us against 126 for the rotation alone, 32768 rows of the 8B shape). A sum of
+// squares is fp32, over the lane's eight elements and then the head's lanes by shuffles; one
+// that leaves fp32's range is taken again from x 2^-70. Only the result is rounded.
+template <typename T, int D, int PIECE>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 2) norm_rope_append_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
+  __shared__ RopeRows<D> s;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int row0 = blockIdx.x * p.tokens;
+  find_rows<D>(p, s);
+
+  const int tok = warp % p.tokens;  // tokens divides WARPS
+  if (s.pos[tok] < 0) return;
+  const int n_kv = p.cache.n_kv, step = WARPS / p.tokens * HPW;
+  const int c = lane % LPH, half = p.rope.rotary_dim / 2;
+  const int first = warp / p.tokens * HPW + lane / LPH;  // the lane's first head
+  const int64_t row = row0 + tok;
+  const uint32_t crow = s.row[tok];
+  const unsigned mine = (LPH == 8 ? 0xffu : 0xffffu) << (lane / LPH * LPH);  // a head's lanes
+  // pieces as above; the pairs behind rotary_dim turn by the angle 0
+  constexpr int N = PIECE, FIRST = N == 8 ? 1 : 4 / N;
+  int at[8 / N];
+  if constexpr (N == 8) {
+    at[0] = 8 * c;
+  } else {
+#pragma unroll
+    for (int i = 0; i < FIRST; ++i) {
+      const int pair = 4 * c + N * i;
+      at[i] = pair < half ? pair : 2 * pair;
+      at[i + FIRST] = pair < half ? half + pair : 2 * pair + N;
+    }
+  }
+  constexpr auto left = [](int j) { return N == 8 ? 2 * j : j; };       // of the lane's pair j
+  constexpr auto right = [](int j) { return N == 8 ? 2 * j + 1 : j + 4; };
+
+  unsigned long long turn[2][4];  // of pairs 0, 1 and 2, 3: v cos, -w sin, v sin, w cos
+  auto put_together = [&](const uint16_t* weights) {
+    uint32_t w[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};  // ones
+    if (weights) {
+#pragma unroll
+      for (int i = 0; i < 8 / N; ++i) load<N>(weights + at[i], w, N * i);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const float2 x = s.cs[tok][4 * c + j], y = s.cs[tok][4 * c + j + 1];
+      const float v0 = elem<uint16_t>(w, left(j)), v1 = elem<uint16_t>(w, left(j + 1));
+      const float w0 = elem<uint16_t>(w, right(j)), w1 = elem<uint16_t>(w, right(j + 1));
+      turn[j / 2][0] = pack2(v0 * x.x, v1 * y.x);
+      turn[j / 2][1] = pack2(-w0 * x.y, -w1 * y.y);
+      turn[j / 2][2] = pack2(v0 * x.y, v1 * y.y);
+      turn[j / 2][3] = pack2(w0 * x.x, w1 * y.x);
+    }
+  };
+  // the head in x, normalised and turned, to dst
+  auto finish = [&](const uint32_t* x, auto* dst) {
+    unsigned long long a[2], b[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      a[j] = pack2(elem<T>(x, left(2 * j)), elem<T>(x, left(2 * j + 1)));
+      b[j] = pack2(elem<T>(x, right(2 * j)), elem<T>(x, right(2 * j + 1)));
+    }
+    auto squares = [&] {
+      unsigned long long sum = mul2(a[0], a[0]);
+      ffma2(sum, b[0], b[0]);
+      ffma2(sum, a[1], a[1]);
+      ffma2(sum, b[1], b[1]);
+      const float2 z = unpack2(sum);
+      float t = z.x + z.y;
+#pragma unroll
+      for (int d = 1; d < LPH; d *= 2) t += __shfl_xor_sync(mine, t, d);
+      return t * (1.f / D);
+    };
+    float mean = squares(), eps = p.eps;
+    if (!(mean < INFINITY)) {
+      const unsigned long long small = pack2(0x1p-70f, 0x1p-70f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) a[j] = mul2(a[j], small), b[j] = mul2(b[j], small);
+      mean = squares();
+      eps = 0.f;  // below a rounding of a mean of 2^121 and more
+    }
+    const float f = rsqrtf(mean + eps);
+    const unsigned long long f2 = pack2(f, f);
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      a[j] = mul2(a[j], f2), b[j] = mul2(b[j], f2);
+      unsigned long long l = mul2(a[j], turn[j][0]), r = mul2(a[j], turn[j][2]);
+      ffma2(l, b[j], turn[j][1]);
+      ffma2(r, b[j], turn[j][3]);
+      const float2 y = unpack2(l), z = unpack2(r);
+      o[left(2 * j)] = y.x, o[left(2 * j + 1)] = y.y;
+      o[right(2 * j)] = z.x, o[right(2 * j + 1)] = z.y;
+    }
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) store<N>(dst + at[i], o + N * i);
+  };
+  uint32_t x[U][2 * sizeof(T)];
+  auto fetch = [&](uint32_t* x, const T* src) {
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) load<N>(src + at[i], x, N * i);
+  };
+
+  put_together(p.q_norm);
+  const T* q = (const T*)p.q + row * p.qs;
+  T* out = (T*)p.q_out + row * p.os;
+  for (int h = first; h < p.nh; h += U * step) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * step < p.nh) fetch(x[u], q + (h + u * step) * D);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * step < p.nh) finish(x[u], out + (h + u * step) * D);
+  }
+  if (crow == kNoRow) return;
+  put_together(p.k_norm);
+  const T *k = (const T*)p.k + row * p.ks, *v = (const T*)p.v + row * p.vs;
+  for (int h = first; h < n_kv; h += U / 2 * step) {
+#pragma unroll
+    for (int u = 0; u < U / 2; ++u) {
+      const int g = h + u * step;
+      if (g < n_kv) fetch(x[u], k + g * D), fetch(x[u + U / 2], v + g * D);
+    }
+#pragma unroll
+    for (int u = 0; u < U / 2; ++u) {
+      const int g = h + u * step;
+      if (g >= n_kv) continue;
+      const size_t to = ((size_t)crow + (size_t)g * p.cache.block_size) * D;
+      finish(x[u], p.k_cache + to);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = elem<T>(x[u + U / 2], j);
+#pragma unroll
+      for (int i = 0; i < 8 / N; ++i) store<N>(p.v_cache + to + at[i], o + N * i);
+    }
+  }
+}
+
+template <typename T, int D, int PIECE, bool NORM>
 void launch_rope(const RopeParams& p, cudaStream_t st) {
   const dim3 grid((p.rows + p.tokens - 1) / p.tokens);
+  if constexpr (NORM) norm_rope_append_kernel<T, D, PIECE><<<grid, kRopeThreads, 0, st>>>(p);
+  else rope_append_kernel<T, D, PIECE><<<grid, kRopeThreads, 0, st>>>(p);
+}
+template <typename T, int D, bool NORM>
+void launch_rope(const RopeParams& p, cudaStream_t st) {
   const int half = p.rope.rotary_dim / 2;
-  if (p.rope.interleaved) rope_append_kernel<T, D, 8, NORM><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (half % 4 == 0) rope_append_kernel<T, D, 4, NORM><<<grid, kRopeThreads, 0, st>>>(p);
-  else if (half % 2 == 0) rope_append_kernel<T, D, 2, NORM><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_append_kernel<T, D, 1, NORM><<<grid, kRopeThreads, 0, st>>>(p);
+  if (p.rope.interleaved) launch_rope<T, D, 8, NORM>(p, st);
+  else if (half % 4 == 0) launch_rope<T, D, 4, NORM>(p, st);
+  else if (half % 2 == 0) launch_rope<T, D, 2, NORM>(p, st);
+  else launch_rope<T, D, 1, NORM>(p, st);
 }
 
 // mk_rope_append and, with NORM, mk_norm_rope_append: the checks that they share, and

@@ -52,6 +52,18 @@ __device__ __forceinline__ int clamped(const int32_t* p, int b, int hi) {
   return p == nullptr ? hi : min(max(__ldg(p + b), 0), hi);
 }
 
+// two-wide arithmetic
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long sum2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // The launch that depends on this one may be scheduled; its griddep_wait still
 // waits until this grid has completed and its writes are visible.
 __device__ __forceinline__ void griddep_launch() {
