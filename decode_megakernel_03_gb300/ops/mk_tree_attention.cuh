@@ -28,6 +28,7 @@ struct Share;
 struct AttnParams {
   using Line = mk::Line;
   using Share = mk::Share;
+  static constexpr bool kMixed = false;
   CacheView cache;
   const uint16_t *k, *v;
   const void* q;
@@ -91,6 +92,7 @@ __device__ __forceinline__ void work_line(const AttnParams& p, Line& line) {
   __syncwarp();
 }
 
+__device__ __forceinline__ void put_plans(const AttnParams&, const Line&) {}
 __device__ __forceinline__ int all_places(const AttnParams& p, const Line& line) {
   return line.prefix[p.B];
 }
@@ -190,6 +192,13 @@ __device__ __forceinline__ bool is_final(const Share& sh) { return sh.n == sh.nt
 __device__ __forceinline__ size_t share_slot(const AttnParams& p, int group, const Share& sh, int rt,
                                              int local, int) {
   return part_slot(p, group, sh.begins, rt) * p.row_tile + local;
+}
+
+// columns c to c + 3 and, behind them, c + 4 to c + 7 of a row of the workspace; `step` vectors on
+// the next eight
+__device__ __forceinline__ float4* part_place(const AttnParams& p, size_t slot, int D, int c, int& step) {
+  step = 2;
+  return reinterpret_cast<float4*>(p.part_o + slot * D + c);
 }
 
 // ---- asynchronous 16-byte copies ---------------------------------------------------

@@ -47,7 +47,7 @@
 // when its copies and products in flight have.
 //
 // P is the call: AttnParams or PrefixParams (mk_prefix_attention.cu), which bring their
-// line of work (P::Line, work_line, all_places, next_share) and say where a share's keys and rows
+// line of work (P::Line, work_line, all_places, next_share, put_plans) and say where a share's keys and rows
 // are: first_slot, first_row, row_there, row_node, row_offset, is_final, share_slot.
 #pragma once
 
@@ -216,6 +216,15 @@ struct Layout {
   static constexpr int kBytes = kQ + kBufs * kBuf + 1024;  // 1024: alignment of the base
 };
 
+// Whether a share's rows are two blocks, a stream each. A call may mix shares of both kinds (P::kMixed):
+// kTwo's shares of up to 128 rows are then taken as kOne's are.
+template <int KIND, class P>
+__device__ __forceinline__ bool two_blocks(const typename P::Share& sh) {
+  if constexpr (KIND != kTwo) return false;
+  else if constexpr (P::kMixed) return sh.rows - first_row(sh) > 128;
+  else return true;
+}
+
 struct Shared {
   uint64_t full[8], empty[8];
   uint64_t s_full[2];              // a stream's scores are in tensor memory
@@ -278,8 +287,6 @@ __device__ __forceinline__ void load_role(const P& p, Shared& sm, const typename
                                           uint32_t ring, uint8_t* ring_ptr, int u_begin, int u_end,
                                           int rt) {
   using Lay = Layout<D, KIND>;
-  constexpr bool TWO = Lay::TWO;
-  constexpr int LEAD = TWO ? 1 : 2;      // K tiles ahead of V
   constexpr int CPR = D / 8, RPW = 32 / CPR;
   constexpr int kLoadRows = kKeys / kLoadWarps;  // keys of a tile that a warp takes
   const int lw = threadIdx.x / 32 - kLoadWarp, lane = threadIdx.x % 32;
@@ -297,8 +304,10 @@ __device__ __forceinline__ void load_role(const P& p, Shared& sm, const typename
       const uint32_t row = cache_row(p.cache, sh.b, slot);
       return row == kNoRow ? row : row + (uint32_t)sh.g * p.cache.block_size;
     };
-    // rows of the tile whose K is next, of the LEAD tiles before it (V is to come)
-    uint32_t next = row_of(0), held[LEAD] = {};
+    const bool two = two_blocks<KIND, P>(sh);
+    const int lead = two ? 1 : 2;          // K tiles ahead of V
+    // rows of the tile whose K is next, of the `lead` tiles before it (V is to come)
+    uint32_t next = row_of(0), held[2] = {};
 
     auto copy = [&](const uint16_t* pool, uint32_t rows) {
       const uint32_t base = ring + buf * Lay::kBuf + (c / 8) * (kKeys * 128);
@@ -327,7 +336,7 @@ __device__ __forceinline__ void load_role(const P& p, Shared& sm, const typename
       if (++buf == Lay::kBufs) buf = 0, ++round;
     };
 
-    for (int j = -LEAD; j < sh.n; ++j) {
+    for (int j = -lead; j < sh.n; ++j) {
       if (j >= 0) {
         // the share's list of odd values is free again (the share before last is
         // written). For every share, whether it has odd values or not: a parity tells
@@ -370,9 +379,8 @@ __device__ __forceinline__ void load_role(const P& p, Shared& sm, const typename
         }
         advance();
       }
-#pragma unroll
-      for (int i = 0; i + 1 < LEAD; ++i) held[i] = held[i + 1];
-      if (const int t = j + LEAD; t < sh.n) {
+      if (!two) held[0] = held[1];
+      if (const int t = j + lead; t < sh.n) {
         const uint32_t there = __ballot_sync(0xffffffffu, next != kNoRow);
         wait(&sm.empty[buf], round + 1);
         if (lane == 0) sm.mask[tile_no % kMasks][lw] = there;
@@ -380,7 +388,8 @@ __device__ __forceinline__ void load_role(const P& p, Shared& sm, const typename
         cp_async_arrive(&sm.full[buf]);
         advance();
         ++tile_no;
-        held[LEAD - 1] = next;
+        if (two) held[0] = next;
+        else held[1] = next;
         next = row_of(t + 1);
       }
     }
@@ -401,7 +410,6 @@ __device__ __forceinline__ void mma_role(const P& p, Shared& sm, const typename 
                                          uint32_t q_smem, uint32_t ring, uint32_t tmem, int u_begin,
                                          int u_end, int rt) {
   using Lay = Layout<D, KIND>;
-  constexpr bool TWO = Lay::TWO;
   constexpr uint32_t kScores = instruction(kKeys, false), kValues = instruction(D, true);
   Waiter wait(sm);
   uint32_t buf = 0, round = 0;
@@ -410,10 +418,11 @@ __device__ __forceinline__ void mma_role(const P& p, Shared& sm, const typename 
   int u = u_begin;
   typename P::Share sh;
   // S of stream s from the K tile in buffer `at`; free: it is not needed again
+  bool two = false;  // of the share
   auto scores = [&](int s, uint32_t at, bool free) {
     if (elect_one()) {
       const uint64_t k = operand(ring + at * Lay::kBuf, 16);
-      const uint64_t q = operand(q_smem + (TWO ? s * 128 * D * 2 : 0), 16);
+      const uint64_t q = operand(q_smem + (two ? s * 128 * D * 2 : 0), 16);
 #pragma unroll
       for (int part = Lay::PARTS - 1; part >= 0; --part)  // the smallest part first
 #pragma unroll
@@ -474,7 +483,8 @@ __device__ __forceinline__ void mma_role(const P& p, Shared& sm, const typename 
     wait(&sm.q_full, share);
     fence_async_smem();
     tc_fence_after();
-    if constexpr (TWO) {
+    two = two_blocks<KIND, P>(sh);
+    if (two) {
       uint32_t k_at = take(), v_at = 0;
 #pragma unroll 1
       for (int i = -2; i < 2 * sh.n; ++i) {  // stream i & 1: products of tile i / 2, then the next scores
@@ -519,6 +529,8 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t v, int from) {
 // The nodes that node `t` sees (t < 64, -1: none), by doubling inside the warp:
 // lane l holds nodes l and l + 32, `up` the next ancestor behind `seen`.
 __device__ __forceinline__ uint64_t nodes_seen(const AttnParams& p, int b, int count, int t) {
+  if (count <= 1) return t == 0 ? 1 : 0;  // no tree: nothing to read
+  if (!p.parents) return t < 0 ? 0 : (2ull << t) - 1;
   const int lane = threadIdx.x % 32;
   uint64_t seen[2];
   int up[2];
@@ -527,7 +539,7 @@ __device__ __forceinline__ uint64_t nodes_seen(const AttnParams& p, int b, int c
     const int n = lane + 32 * h;
     int x = -1;
     if (n < count) {
-      x = p.parents ? __ldg(p.parents + (size_t)b * p.T + n) : n - 1;
+      x = __ldg(p.parents + (size_t)b * p.T + n);
       if (x < 0 || x >= n) x = -1;
     }
     up[h] = x;
@@ -552,33 +564,57 @@ __device__ __forceinline__ uint64_t nodes_seen(const AttnParams& p, int b, int c
   return t < 0 ? 0 : t < 32 ? a : c;
 }
 
-// The queries of row r of a row block into shared memory (columns 8 first to 8 end),
-// swizzled, in PARTS bf16 parts; a row that is not there is zero.
-template <int D, int PARTS, class P>
-__device__ __forceinline__ void load_query(const P& p, const typename P::Share& sh, int row, bool live,
-                                           int r, uint8_t* block, int first = 0, int end = D / 8) {
-  uint8_t* dst = block + r * 128;
-  const int64_t off = live ? row_offset(p, sh, row, D, p.qs) : 0;
-#pragma unroll 4
-  for (int c = first; c < end; ++c) {
-    uint4 w[PARTS];
-    if constexpr (PARTS == 1) {
-      w[0] = __ldg(reinterpret_cast<const uint4*>((const uint16_t*)p.q + off) + c);
-    } else {
-      const float4* src = reinterpret_cast<const float4*>((const float*)p.q + off) + 2 * c;
-      const float4 a = __ldg(src), b = __ldg(src + 1);
-      uint32_t x[4][PARTS];
-      split(a.x, a.y, x[0]);
-      split(a.z, a.w, x[1]);
-      split(b.x, b.y, x[2]);
-      split(b.z, b.w, x[3]);
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) w[q] = make_uint4(x[0][q], x[1][q], x[2][q], x[3][q]);
+// The queries of rows `row` to `row` + n - 1 into rows 0 to n - 1 of a block of shared memory
+// (COPIES of them, 32 rows apart), swizzled, in PARTS bf16 parts, by THREADS threads
+// of which this is number `tid`: lanes that follow one another take 16 bytes that do (a row
+// for each thread took 3200 cycles, of a few rows as of 128). Rows that are not there keep
+// what the block held: what comes of them goes nowhere.
+template <int D, int PARTS, int COPIES, int THREADS, class P>
+__device__ __forceinline__ void load_queries(const P& p, const typename P::Line& line,
+                                             const typename P::Share& sh, int row, int n, int tid,
+                                             uint8_t* block) {
+  constexpr int CPR = D / 8;
+  auto place = [](int r, int c) { return r * 128 + (c / 8) * (128 * 128) + (((c % 8) ^ (r & 7)) * 16); };
+  if constexpr (PARTS == 1) {
+    const uint32_t to = smem_u32(block);
+    for (int i = tid; i < n * CPR; i += THREADS) {
+      const int r = i / CPR, c = i % CPR;
+      if (row_there(p, line, sh, row + r))
+        cp_async16(to + place(r, c), (const uint16_t*)p.q + row_offset(p, sh, row + r, D, p.qs) + 8 * c);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    constexpr int U = COPIES == 1 ? 2 : 1;  // pieces in flight
+    for (int i0 = tid; i0 < n * CPR; i0 += U * THREADS) {
+      uint4 w[U][2];
+      bool there[U];
 #pragma unroll
-    for (int q = 0; q < PARTS; ++q)
-      *reinterpret_cast<uint4*>(dst + q * 128 * D * 2 + (c / 8) * (128 * 128) +
-                                (((c % 8) ^ (r & 7)) * 16)) = live ? w[q] : make_uint4(0, 0, 0, 0);
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * THREADS, r = i / CPR;
+        there[u] = i < n * CPR && row_there(p, line, sh, row + r);
+        if (!there[u]) continue;
+        const float* src = (const float*)p.q + row_offset(p, sh, row + r, D, p.qs) + 8 * (i % CPR);
+        w[u][0] = __ldg(reinterpret_cast<const uint4*>(src));
+        w[u][1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!there[u]) continue;
+        const int i = i0 + u * THREADS;
+        uint32_t part[4][PARTS];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          split(__uint_as_float(w[u][h].x), __uint_as_float(w[u][h].y), part[2 * h]);
+          split(__uint_as_float(w[u][h].z), __uint_as_float(w[u][h].w), part[2 * h + 1]);
+        }
+#pragma unroll
+        for (int k = 0; k < COPIES; ++k)
+#pragma unroll
+          for (int q = 0; q < PARTS; ++q)
+            *reinterpret_cast<uint4*>(block + place(i / CPR + 32 * k, i % CPR) + q * 128 * D * 2) =
+                make_uint4(part[0][q], part[1][q], part[2][q], part[3][q]);
+      }
+    }
   }
   fence_async_smem();
 }
@@ -717,10 +753,11 @@ __device__ __forceinline__ void put_columns(const P& p, const typename P::Share&
                             bf16x2_rn(y[8 * e + 4], y[8 * e + 5]), bf16x2_rn(y[8 * e + 6], y[8 * e + 7]));
     }
   } else if (live) {
-    float4* dst = reinterpret_cast<float4*>(p.part_o + slot * D + c);
+    int step;
+    float4* dst = part_place(p, slot, D, c, step);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      dst[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+      dst[e / 2 * step + e % 2] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
   }
   __syncwarp();
 }
@@ -750,14 +787,11 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
                                              uint8_t* q_ptr, uint32_t tmem, int u_begin,
                                              int u_end, int rt, int group) {
   using Lay = Layout<D, KIND>;
-  constexpr bool TWO = Lay::TWO;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int stream = warp / 4, r = (warp % 4) * 32 + lane;  // row of the stream's block
   const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
   const uint32_t t_s = tmem + lanes + stream * Lay::kScoreStep;
   const uint32_t t_o = tmem + lanes + Lay::kOut + stream * D;
-  const int block_rows = TWO ? p.row_tile / 2 : 128;       // rows of a stream's block
-  const int local = TWO ? stream * block_rows + r : r;     // row of the row tile
   const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2);
   Waiter wait(sm);
   uint32_t s_uses = 0, tile_no = 0;
@@ -765,17 +799,22 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
   typename P::Share sh;
   for (uint32_t share = 0; next_share(p, line, u_begin, u_end, u, sh);) {
     if (rt * p.row_tile >= sh.rows) continue;
+    const bool two = two_blocks<KIND, P>(sh);
+    const int block_rows = two ? p.row_tile / 2 : 128;       // rows of a stream's block
+    const int local = two ? stream * block_rows + r : r;     // row of the row tile
     const int row = first_row(sh) + rt * p.row_tile + local;
     const bool live = r < block_rows && row_there(p, line, sh, row);
     const bool warp_live = __any_sync(0xffffffffu, live);
-    if (TWO || stream == 0)
-      load_query<D, 1>(p, sh, row, live, r, q_ptr + (TWO ? stream * 128 * D * 2 : 0));
+    if (two)
+      load_queries<D, 1, 1, 128>(p, line, sh, row - r, block_rows, r, q_ptr + stream * 128 * D * 2);
+    else
+      load_queries<D, 1, 1, 256>(p, line, sh, row - r, min(128, sh.rows - (row - r)), threadIdx.x, q_ptr);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full);
     const uint64_t seen = nodes_seen(p, sh.b, sh.count, live ? row_node(p, sh, row) : -1);
 
     float m = -INFINITY, l = 0.f;  // m: the reference, scaled by log2(e)
-    for (int j = TWO ? 0 : stream; j < sh.n; j += TWO ? 1 : 2) {
+    for (int j = two ? 0 : stream; j < sh.n; j += two ? 1 : 2) {
       wait(&sm.s_full[stream], s_uses++);
       tc_fence_after();
       if (warp_live) {
@@ -783,7 +822,7 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
         const Sight v = sight_of(sm.mask[(tile_no + j) % kMasks], sh.start - first_slot(sh) - (sh.k0 + j) * kKeys, seen);
         const float top = read_scores(t_s, v.some, v.bits, x);
         const float keep = move_reference(top * p.scale_log2, m, l);
-        const int before = TWO ? j : j / 2;  // tiles already in O
+        const int before = two ? j : j / 2;  // tiles already in O
         if (before > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -831,16 +870,16 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
     tile_no += sh.n;
 
     // ---- the share's rows
-    if (!TWO && stream == 1) {
+    if (!two && stream == 1) {
       sm.ml[r][0] = m;
       sm.ml[r][1] = l;
     }
     wait(&sm.o_full, share);
     tc_fence_after();
-    if (!TWO) named_bar(1, 32 * kSoftWarps);
-    if ((TWO || stream == 0) && warp_live) {
+    if (!two) named_bar(1, 32 * kSoftWarps);
+    if ((two || stream == 0) && warp_live) {
       float f0 = 1.f, f1 = 0.f;  // factors of the streams' shares (one row block)
-      if (!TWO) {
+      if (!two) {
         const float m1 = sm.ml[r][0], l1 = sm.ml[r][1];
         const float both = fmaxf(m, m1);
         f0 = l == 0.f ? 0.f : fast_exp2(m - both);
@@ -851,7 +890,7 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
         f0 = 0.f;
       }
       if (wait_failed(sm)) l = NAN;
-      const bool second = !TWO && sh.n > 1;  // stream 1 had a tile
+      const bool second = !two && sh.n > 1;  // stream 1 had a tile
       const size_t slot = share_slot(p, group, sh, rt, local, row);
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -905,7 +944,9 @@ __device__ __forceinline__ void exact_role(const P& p, Shared& sm, const typenam
     if (rt * p.row_tile >= sh.rows) continue;
     const int row = first_row(sh) + rt * p.row_tile + (FEW ? lane : r);
     const bool live = copy < 3 && row_there(p, line, sh, row), warp_live = __any_sync(0xffffffffu, live);
-    load_query<D, 3>(p, sh, row, live, r, q_ptr, half * (D / 16), (half + 1) * (D / 16));
+    const int row0 = row - (FEW ? lane : r);
+    load_queries<D, 3, FEW ? 3 : 1, 256>(p, line, sh, row0, min(FEW ? 32 : 128, sh.rows - row0),
+                                         threadIdx.x, q_ptr);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_full);
     const uint64_t seen = nodes_seen(p, sh.b, sh.count, live ? row_node(p, sh, row) : -1);
@@ -1085,6 +1126,7 @@ tree_attention_tc_kernel(const __grid_constant__ P p) {
     load_role<D, KIND, P>(p, sm, line, smem_u32(ring_ptr), ring_ptr, u_begin, u_end, rt);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kMmaWarp + 1) put_plans(p, line);
     if (warp == kMmaWarp)
       mma_role<D, KIND, P>(p, sm, line, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
   }
