@@ -130,7 +130,7 @@ __device__ __forceinline__ float load1(const T* p) {
   else return bf16f(__ldg(reinterpret_cast<const uint16_t*>(p)));
 }
 // a drafter's probability: NaN and negative ones are 0
-__device__ __forceinline__ float probability(float q) { return q > 0.f ? q : 0.f; }
+__device__ __forceinline__ float probability(float q) { return fmaxf(q, 0.f); }
 
 // A row's softmax at a temperature: weights relative to the largest logit. A NaN or
 // -inf has none; the largest has 1, also where it is infinite or the temperature tiny.
@@ -165,9 +165,33 @@ struct Softmax {
       const float2 z = unpack2(sum);
       if (z.x + z.y < INFINITY) return z.x + z.y;  // else one is NaN
     }
+    return slow_weights(v, i, w);
+  }
+  template <typename L>
+  __device__ __noinline__ float slow_weights(const Eight<L> v, int i, float (&w)[E]) const {
     float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) sum += w[e] = weight(v[e], i + e);
+    return sum;
+  }
+  // of U groups: their sum
+  template <int U, typename G>
+  __device__ __forceinline__ float sum_of(const G (&x)[U]) const {
+    if (plain) {
+      unsigned long long sum[2] = {0, 0};
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 w = quick(x[u].v[e], x[u].v[e + 1]);
+          sum[e / 2 % 2] = sum2(sum[e / 2 % 2], pack2(w.x, w.y));
+        }
+      const float2 z = unpack2(sum2(sum[0], sum[1]));
+      if (z.x + z.y < INFINITY) return z.x + z.y;
+    }
+    float sum = 0.f, w[E];
+#pragma unroll
+    for (int u = 0; u < U; ++u) sum += slow_weights(x[u].v, 0, w);
     return sum;
   }
 };
@@ -234,27 +258,24 @@ struct Rows<T> {
   }
 };
 
-// The thread's groups of eight values in ascending order, U at a time: take(i, group). The next
-// U are loaded while the ones before are taken.
+// The thread's groups of eight values in ascending order, U at a time, kStride apart:
+// take(i, groups). The next U are loaded while the ones before are taken; what lies behind
+// the end is `fill`.
+constexpr int kStride = kThreads * E;
 template <bool VEC, int U, typename R, typename Take>
 __device__ __forceinline__ void over_values(int first, int hi, const R& rows, Take take) {
-  constexpr int kStride = kThreads * E;
   typename R::Group next[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (first + u * kStride < hi) rows.template load<VEC>(first + u * kStride, hi, next[u]);
+  for (int u = 0; u < U; ++u) rows.template load<VEC>(first + u * kStride, hi, next[u]);
 #pragma unroll 1
-  for (int i0 = first; i0 < hi; i0 += U * kStride) {
+  for (int i = first; i < hi; i += U * kStride) {
     typename R::Group now[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       now[u] = next[u];
-      const int i = i0 + (U + u) * kStride;
-      if (i < hi) rows.template load<VEC>(i, hi, next[u]);
+      if (i + U * kStride < hi) rows.template load<VEC>(i + (U + u) * kStride, hi, next[u]);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u * kStride < hi) take(i0 + u * kStride, now[u]);
+    take(i, now);
   }
 }
 
@@ -265,10 +286,15 @@ __device__ __forceinline__ void over_values(int first, int hi, const R& rows, Ta
 // block 0 alone reads what decides the walk beside the sums (the tree, the random numbers,
 // the children's logits, the temperature) and hands it on, beside the others' work, so that all
 // blocks take the same way to the same barriers whatever the inputs are.
-// Few sequences are bound by the chain of a step, about 5500 cycles with 16 blocks on a
-// row of 128256 values: 2300 until the part's sum is there (memory, then eight values at a
-// time), 500 to hand it on, 1100 at the barrier, 1000 to add up the parts, 500 to decide.
-// Copies to shared memory ahead of the sums (16 bytes a thread each) took 4300 for the 2300.
+// Bound by latency. Few sequences: by the chain of a step, about 5000 cycles with 16 blocks on a
+// row of 128256 values: 1900 until the part's sum is there (memory, then eight values at a
+// time), 500 to hand it on, 1300 at the barrier, 1000 to add up the parts, 500 to decide; 8
+// trees of 64, 1 to 6 nodes accepted, take 26 us. Many: by the sequences with the longest
+// chains, whose four blocks have 5700 cycles of a step to read and sum 32064 values each; 64
+// chains of 8, 132 MB of rows, take 52 us, 2.5 TB/s. Measured and slower: copies to shared
+// memory ahead of the sums, 16 bytes a thread each (4300 cycles for the 1900); two groups of
+// values at a time in the race or the residual's sum (registers; 59 us); 512 threads a block
+// (clusters of 16 that no longer fit all at once: 46 us for 8 sampled trees instead of 32).
 template <typename L, typename Q, bool VEC>
 __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ Shared sm;
@@ -337,28 +363,31 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
     // ---- the node's softmax, and its children
     row = (const L*)p.logits + (base + cur) * p.logits_stride;
     draft = (const Q*)p.draft + (base + cur) * p.draft_stride;
+    // (more than two rounds of loads: into the L2 cache at once, 7200 -> 5700 cycles)
+    if (step > 0 && p.span > 16 / (int)sizeof(L) * kStride) fetch_part(row, sizeof(L));
     f.only = -1;
     f.top = -INFINITY;
     float sum = 0.f;
     int at = INT_MAX;  // heat not above 0: the first index of the largest
     const Rows<L> values{row, -INFINITY};
     if (heat > 0.f) {
-      over_values<VEC, 8 / sizeof(L)>(first, hi, values, [&](int, const auto& x) {
-        const float top = largest(x.v);
+      constexpr int U = 8 / sizeof(L);
+      over_values<VEC, U>(first, hi, values, [&](int, const auto& x) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, largest(x[u].v));
         if (top > f.top) {
           sum = sum > 0.f ? sum * fast_exp2((f.top - top) * f.k) : 0.f;
           f.top = top;
           f.set_plain();
         }
-        if (f.top == -INFINITY) return;
-        float w[E];
-        sum += f.weights(x.v, 0, w);
+        if (f.top > -INFINITY) sum += f.sum_of(x);
       });
     } else {
       over_values<VEC, 1>(first, hi, values, [&](int i, const auto& x) {
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          if (x.v[e] > f.top) f.top = x.v[e], at = i + e;
+          if (x[0].v[e] > f.top) f.top = x[0].v[e], at = i + e;
       });
       if (f.top == -INFINITY) at = INT_MAX;
     }
@@ -473,9 +502,9 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
         float sum = 0.f;
         over_values<VEC, 1>(first, hi, Rows<L, Q>{row, -INFINITY, {draft, 0.f}}, [&](int i, const auto& x) {
           float w[E];
-          f.weights(x.v, i, w);
+          f.weights(x[0].v, i, w);
 #pragma unroll
-          for (int e = 0; e < E; ++e) sum += fmaxf(w[e] * f.inv - c * probability(x.rest.v[e]), 0.f);
+          for (int e = 0; e < E; ++e) sum += fmaxf(w[e] * f.inv - c * probability(x[0].rest.v[e]), 0.f);
         });
         exchange(make_uint2(__float_as_uint(warp_sum(sum)), 0));
         float all = 0.f;
@@ -504,18 +533,22 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
     if (!all) fetch_part(draft, sizeof(Q));
     float best = 0.f;
     int at = -1;
-    // (the first of the largest scores)
-    auto race = [&](int i, const float(&w)[E], const Eight<float>& e) {
+    // (the first of the largest scores: a thread meets its values in ascending order)
+    auto race = [&](int i, float(&w)[E], const Eight<float>& e) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const float score = __fdividef(w[j], e[j] > 1e-30f ? fminf(e[j], 1e30f) : 1e-30f);
-        if (score > best) best = score, at = i + j;
+      for (int j = 0; j < E; ++j) w[j] = __fdividef(w[j], fminf(fmaxf(e[j], 1e-30f), 1e30f));
+      const float top = fmaxf(fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), fmaxf(fmaxf(w[4], w[5]), fmaxf(w[6], w[7])));
+      if (top > best) {
+        best = top;
+#pragma unroll
+        for (int j = E - 1; j >= 0; --j)
+          if (w[j] == top) at = i + j;
       }
     };
     if (all) {
       over_values<VEC, 1>(first, hi, Rows<L, float>{row, -INFINITY, {noise, 1.f}}, [&](int i, const auto& x) {
         float w[E];
-        f.weights(x.v, i, w);
+        f.weights(x[0].v, i, w);
         if (!again)
           for (int j = 0; j < gone; ++j) {
             const int d = sm.gone[j] - i;
@@ -523,16 +556,16 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
             for (int e = 0; e < E; ++e)
               if (d == e) w[e] = 0.f;
           }
-        race(i, w, x.rest.v);
+        race(i, w, x[0].rest.v);
       });
     } else {
       const float by = c * __fdividef(1.f, f.inv);  // in units of the weights
       over_values<VEC, 1>(first, hi, Rows<L, Q, float>{row, -INFINITY, {draft, 0.f, {noise, 1.f}}}, [&](int i, const auto& x) {
         float w[E];
-        f.weights(x.v, i, w);
+        f.weights(x[0].v, i, w);
 #pragma unroll
-        for (int j = 0; j < E; ++j) w[j] -= by * probability(x.rest.v[j]);
-        race(i, w, x.rest.rest.v);
+        for (int j = 0; j < E; ++j) w[j] = fmaf(-by, probability(x[0].rest.v[j]), w[j]);
+        race(i, w, x[0].rest.rest.v);
       });
     }
     {
