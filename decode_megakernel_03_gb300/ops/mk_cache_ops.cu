@@ -114,7 +114,7 @@ __device__ __forceinline__ void store(uint16_t* p, const float* x) {
 
 // ---- rotary positions and append ------------------------------------------------
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeTokens = 4;  // most tokens of a block
 
 struct RopeParams {
@@ -289,26 +289,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 // put together once for a row: a pair (a, b) with weights (v, w) becomes
 //   f (a v cos - b w sin), f (a v sin + b w cos),
 // four products of a weight and an angle that stay in a lane's registers while it goes
-// through its heads (of q, then of k and v), pair by pair in two-wide arithmetic: with the
-// weights and the rotation one after another the instructions, not the bytes, took the
-// time (170 us against 126 for the rotation alone, 32768 rows of the 8B shape). A sum of
+// through its heads (of q, then of k and v), pair by pair in two-wide arithmetic. A sum of
 // squares is fp32, over the lane's eight elements and then the head's lanes by shuffles; one
 // that leaves fp32's range is taken again from x 2^-70. Only the result is rounded.
+// Bound by the bytes, with less room to wait for them than the rotation alone has: 32768 rows
+// of the 8B shape, bf16 in halves, 805 MB, take 131 us, 6.1 TB/s. Weights and rotation one
+// after another: 170; blocks of 256 threads: 142, and 153 with as many registers as it
+// would like; sixteen elements a lane: 155 to 171. 600 rows take 6 us, a launch's latency and
+// that of a row's position, angle and queries.
 template <typename T, int D, int PIECE>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 2) norm_rope_append_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 7 : 4) norm_rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
   __shared__ RopeRows<D> s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row0 = blockIdx.x * p.tokens;
-  find_rows<D>(p, s);
-
   const int tok = warp % p.tokens;  // tokens divides WARPS
-  if (s.pos[tok] < 0) return;
   const int n_kv = p.cache.n_kv, step = WARPS / p.tokens * HPW;
   const int c = lane % LPH, half = p.rope.rotary_dim / 2;
   const int first = warp / p.tokens * HPW + lane / LPH;  // the lane's first head
   const int64_t row = row0 + tok;
-  const uint32_t crow = s.row[tok];
   const unsigned mine = (LPH == 8 ? 0xffu : 0xffffu) << (lane / LPH * LPH);  // a head's lanes
   // pieces as above; the pairs behind rotary_dim turn by the angle 0
   constexpr int N = PIECE, FIRST = N == 8 ? 1 : 4 / N;
@@ -325,6 +324,25 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 2) norm_rop
   }
   constexpr auto left = [](int j) { return N == 8 ? 2 * j : j; };       // of the lane's pair j
   constexpr auto right = [](int j) { return N == 8 ? 2 * j + 1 : j + 4; };
+
+  uint32_t x[U][2 * sizeof(T)];
+  auto fetch = [&](uint32_t* x, const T* src) {
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) load<N>(src + at[i], x, N * i);
+  };
+  const T* q = (const T*)p.q + row * p.qs;
+  auto fetch_queries = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * step < p.nh) fetch(x[u], q + (h + u * step) * D);
+  };
+  // the first queries are on their way while the row's position and angles are found, where
+  // every row is there
+  const bool early = p.counts == nullptr && row < p.rows;
+  if (early) fetch_queries(first);
+  find_rows<D>(p, s);
+  if (s.pos[tok] < 0) return;
+  const uint32_t crow = s.row[tok];
 
   unsigned long long turn[2][4];  // of pairs 0, 1 and 2, 3: v cos, -w sin, v sin, w cos
   auto put_together = [&](const uint16_t* weights) {
@@ -387,19 +405,10 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 2) norm_rop
 #pragma unroll
     for (int i = 0; i < 8 / N; ++i) store<N>(dst + at[i], o + N * i);
   };
-  uint32_t x[U][2 * sizeof(T)];
-  auto fetch = [&](uint32_t* x, const T* src) {
-#pragma unroll
-    for (int i = 0; i < 8 / N; ++i) load<N>(src + at[i], x, N * i);
-  };
-
   put_together(p.q_norm);
-  const T* q = (const T*)p.q + row * p.qs;
   T* out = (T*)p.q_out + row * p.os;
   for (int h = first; h < p.nh; h += U * step) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (h + u * step < p.nh) fetch(x[u], q + (h + u * step) * D);
+    if (!early || h != first) fetch_queries(h);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (h + u * step < p.nh) finish(x[u], out + (h + u * step) * D);
