@@ -12,6 +12,16 @@
 // from the shares of both items by a second kernel (an item that was not cut leaves
 // its sums in a place of its row's own), but where there is no prefix a whole item
 // writes its rows.
+//
+// Measured on the 8B shape, bf16: 64 samples of two documents (32768 and 26215 keys, 256
+// to 2048 own keys, 4 nodes each; 531 MB, 123 GFLOP) 211 us: the prefixes' tiles are
+// bound by the products, which both parts of the weights go through (4400 cycles for two
+// blocks of rows, 3072 of them products), the own keys' by the beginnings and ends of 512
+// items (9000 cycles each) and their tiles (2000). 32 samples behind 8192 keys, 16 to 512
+// own ones (68 MB) 37 us: 4 until a block has its line and the first keys, 21 to 26 for 3
+// to 4 shares, 5 for the join. (The own keys by a kernel at warp level that also joins
+// them with the prefix's sums, started early, took 47 and 250 us: it has the memory to
+// itself only when the products are done.)
 #include <algorithm>
 #include <type_traits>
 
@@ -350,13 +360,13 @@ __global__ void __launch_bounds__(128) prefix_attention_join(const __grid_consta
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   if (joins) {
-    // lane i: where share s0 + i keeps the row (-1: no share, or no key seen in
-    // it), its maximum and sum
-    int64_t at;
+    // lane i: where share s0 + i keeps the row's first columns (a vector of part_o, fewer than
+    // 2^32 of them; kNoRow: no share, or no key seen in it), its maximum and sum
+    uint32_t at;
     float ms, ls;
     auto look = [&](int s0) {
       const int s = s0 + lane;
-      at = -1, ms = -INFINITY, ls = 0.f;
+      at = kNoRow, ms = -INFINITY, ls = 0.f;
       if (s < all) {
         const int which = s < n[0] ? 0 : 1;
         const int group = (which ? g0[1] - n[0] : g0[0]) + s;
@@ -372,9 +382,15 @@ __global__ void __launch_bounds__(128) prefix_attention_join(const __grid_consta
           x = (int64_t)part_slot(p, group, u0 >= t0 - p.extra, 0) * p.row_tile + (which ? local[1] : local[0]);
         }
         const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + x);
-        if (ml.y != 0.f) at = x, ms = ml.x, ls = ml.y;
+        int step;
+        const float4* place = part_place(p, (size_t)x, D, 0, step);
+        if (ml.y != 0.f) at = (uint32_t)(place - reinterpret_cast<const float4*>(p.part_o)), ms = ml.x, ls = ml.y;
       }
     };
+    // the lane's columns of a share whose next eight columns are `step` vectors on
+    const int step0 = n[0] == 1 ? 2 : 2 * p.row_tile, step1 = n[1] == 1 ? 2 : 2 * p.row_tile;
+    const Vec* base = reinterpret_cast<const Vec*>(p.part_o) + lane % (8 / E);
+    const int near0 = lane / (8 / E) * step0, near1 = lane / (8 / E) * step1;
     float m = -INFINITY;
     for (int s0 = 0; s0 < all; s0 += 32) {
       look(s0);
@@ -384,7 +400,7 @@ __global__ void __launch_bounds__(128) prefix_attention_join(const __grid_consta
     for (int d = 16; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     for (int s0 = 0; s0 < all; s0 += 32) {
       if (all > 32) look(s0);  // else the lanes still have it
-      const float f = at < 0 ? 0.f : fast_exp2(ms - m);
+      const float f = at == kNoRow ? 0.f : fast_exp2(ms - m);
       l += ls * f;
       const int here = min(32, all - s0);
       for (int k0 = turn; k0 < here; k0 += U * TURNS) {
@@ -393,15 +409,10 @@ __global__ void __launch_bounds__(128) prefix_attention_join(const __grid_consta
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           const int k = k0 + i * TURNS;
-          const int64_t x = __shfl_sync(0xffffffffu, at, k & 31);
+          const uint32_t x = __shfl_sync(0xffffffffu, at, k & 31);
           w[i] = __shfl_sync(0xffffffffu, f, k & 31);
           v[i] = Vec{};
-          if (k < here && x >= 0) {
-            int step;
-            const float4* from = part_place(p, (size_t)x, D, 0, step);
-            if constexpr (E == 4) v[i] = __ldcg(from + lane / 2 * step + lane % 2);
-            else v[i] = __ldcg(reinterpret_cast<const float2*>(from + lane / 4 * step) + lane % 4);
-          }
+          if (k < here && x != kNoRow) v[i] = __ldcg(base + (size_t)(x + (s0 + k < n[0] ? near0 : near1)) * (4 / E));
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {

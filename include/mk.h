@@ -330,9 +330,10 @@ int mk_schedule_build_steps(const mk_config* cfg, int n_sm, const int32_t* posit
 
 /* What a serving loop needs beside the decode step, on the same caches: a
    tree of drafted tokens verified in one pass (new rows appended with rotary
-   positions, attention of the tree's nodes, greedy acceptance, the accepted
-   rows moved down behind the context), and the pages of a paged cache forked,
-   copied, compacted and freed.
+   positions, attention of the tree's nodes, greedy or sampled acceptance, the
+   accepted rows moved down behind the context), several answers of one prompt
+   served together, and the pages of a paged cache forked, copied, compacted and
+   freed.
 
    These calls take no handle. Beyond the conventions above:
    - mk_last_error(NULL) describes a failure (per host thread).
@@ -432,13 +433,13 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
                    int64_t q_out_stride, const int32_t* starts, const int32_t* parents,
                    const int32_t* counts, void* stream);
 
-/* mk_rope_append for a model that normalises each head of its queries and keys
-   before their rotation: a head x becomes x w / sqrt(mean of x^2 + eps), in fp32,
-   in the same pass; what is rounded is the rotated value only. q_norm, k_norm:
-   DEVICE bf16 [head_dim], 16-byte aligned, shared by the heads; NULL: ones. eps
-   1e-30 to 1. Values pass as they are. A NaN or an infinity in a head of q or k stays with that
-   head. The other arguments and the errors are those of mk_rope_append.
-   (mk_decode_step and the other calls with a handle do not normalise heads.) */
+/* mk_rope_append for a model that normalises each head of its queries and keys before
+   their rotation: a head x becomes x w / sqrt(mean of x^2 + eps), in fp32, in the
+   same pass; only the rotated value is rounded. q_norm, k_norm: DEVICE bf16
+   [head_dim], 16-byte aligned, shared by the heads; NULL: ones. eps 1e-30 to 1. The v
+   rows pass as they are. A NaN or an infinity in a head of q or k stays with that head. The
+   other arguments and the errors are those of mk_rope_append. (mk_decode_step and the
+   other calls with a handle do not normalise heads.) */
 int mk_norm_rope_append(const mk_rope* rope, const void* q_norm, const void* k_norm, float eps,
                         const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
                         int type, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -474,14 +475,14 @@ int mk_tree_attention_workspace(const mk_cache* cache, int batch, int n_tokens, 
 /* mk_tree_attention for a batch whose groups share a prefix (the samples of a prompt,
    mk_pages_fork): the prefix's keys are read once for all sequences of a group.
    first, prefix: DEVICE int32 [n_groups], n_groups 1 to batch. Group i is the
-   sequences from first[i] on, up to the next group's first (the last: to the
-   batch's end); a first below the one before it or outside [0, batch] is taken at the nearest bound, a group
-   may come out empty, and sequences before first[0] share nothing. The slots
-   below prefix[i] (at least 0, at most the smallest starts of the group's sequences that have
-   nodes) hold the same rows for the whole group: those of the group's FIRST sequence are
-   read, the others' table entries for whole pages of them are not. Everything else is
-   as in mk_tree_attention, whose result this is where the group's tables agree,
-   up to the order of its sums.
+   sequences from first[i] on, up to the next group's first (the last: to the batch's
+   end). A first below the one before it or outside [0, batch] is taken at the nearest
+   bound; a group may come out empty; sequences before first[0] share nothing. The
+   slots below prefix[i] (at least 0, at most the smallest starts of those of the
+   group's sequences that have nodes) hold the same rows for the whole group: the rows
+   of the group's FIRST sequence are read for them. Everything else is as in
+   mk_tree_attention, whose result this is where the group's tables agree, up to the
+   order of its sums. Deterministic in the same way.
    Errors: MK_ERR_INVALID (also a workspace below the query's size), MK_ERR_CUDA. */
 int mk_prefix_attention(const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
                         int type, float scale, const void* q, int64_t q_stride, int n_groups,
@@ -513,25 +514,29 @@ int mk_tree_accept_workspace(int batch, int n_tokens, int vocab, size_t* bytes);
 /* Verification of a drafted tree by rejection sampling: what is accepted, and the
    token after it, are distributed as if they had been sampled from the target one
    by one. The arguments of mk_tree_accept, and:
-   temperature (DEVICE fp32 [batch], NULL: 1): a row's probabilities p are the
-   softmax of its logits / temperature; at one that is not above 0, NaN included, the
-   first largest logit has them all. A logit that is NaN or -inf has probability 0.
+   temperature (DEVICE fp32 [batch], NULL: 1): a row's probabilities p are the softmax
+   of its logits / temperature; at one that is not above 0, NaN included, the first
+   largest logit has them all. A logit that is NaN or -inf has probability 0.
    draft (DEVICE `draft_type`, rows as the logits', at draft_stride): row t is the
-   distribution q that the children of node t were each sampled from (values below 0 and
-   NaN count as 0); NULL: the children were proposed without one. uniform (DEVICE fp32 [batch][n_tokens]), the
-   number in [0, 1) by which each node is accepted or not (node 0's is not used; others are taken at the
-   nearer bound, NaN as 0); noise (DEVICE fp32, row b at b * noise_stride): `vocab` numbers of an exponential
-   distribution with mean 1 (taken at 1e-30 below it and NaN, at 1e30 above it).
+   distribution q from which the children of node t were sampled, each by itself
+   (values below 0 and NaN count as 0). NULL: the children were proposed without one,
+   by a rule that does not look at the random numbers below.
+   uniform (DEVICE fp32 [batch][n_tokens]): the number in [0, 1) by which each node
+   is accepted or not (node 0's is not used; others are taken at the nearer bound,
+   NaN as 0).
+   noise (DEVICE fp32, row b at b * noise_stride): `vocab` numbers of an exponential
+   distribution with mean 1 (taken at 1e-30 below that and for NaN, at 1e30 above it).
    From node 0 on, the children of a node are taken in ascending order: child t
-   with token x is accepted if uniform[t] q(x) < r(x), where r is p at first; the
-   walk goes on from it. After a rejection r becomes max(r - q, 0), scaled to sum
-   1 (without draft: r without x, scaled; q(x) is 1 above). Where no child is
-   accepted, next is the index of the largest r / noise (the lowest among equal
-   ones), a sample of r. A token outside [0, vocab) is passed over, and what hangs
-   off it with it. Where rounding leaves nothing of r, next is sampled from p. In a row
-   without a logit above -inf there is no p: nothing is accepted, next is -1. Probabilities and sums
-   are fp32 (2^-20 of their value, differences 2^-20 of what is subtracted): a comparison closer than
-   that may fall either way, the same way each time. Outputs as mk_tree_accept's (path, accepted, next).
+   with token x is accepted if uniform[t] q(x) < r(x), where r is p at first, and the
+   walk goes on from it. After a rejection r becomes max(r - q, 0), scaled to sum 1
+   (without draft: r without x, scaled; q(x) is 1 above). Where no child is accepted,
+   next is the index of the largest r / noise (the lowest among equal ones), which
+   is a sample of r. A token outside [0, vocab) is passed over, and what hangs off it
+   with it. Where rounding leaves nothing of r, next is sampled from p. At a row
+   without a logit above -inf there is no p: the walk ends there and next is -1.
+   Probabilities and sums are fp32, to 2^-16 of their value at worst (differences: of
+   what is subtracted): a comparison closer than that may fall either way, the same
+   way each time. Outputs as mk_tree_accept's path, accepted and next. No workspace.
    Errors: MK_ERR_INVALID, MK_ERR_CUDA. */
 int mk_tree_verify(int batch, int n_tokens, int vocab, int type, const void* logits,
                    int64_t logits_stride, int draft_type, const void* draft, int64_t draft_stride,
