@@ -18,10 +18,10 @@
 // bound by the products, which both parts of the weights go through (4400 cycles for two
 // blocks of rows, 3072 of them products), the own keys' by the beginnings and ends of 512
 // items (9000 cycles each) and their tiles (2000). 32 samples behind 8192 keys, 16 to 512
-// own ones (68 MB) 37 us: 4 until a block has its line and the first keys, 21 to 26 for 3
-// to 4 shares, 5 for the join. (The own keys by a kernel at warp level that also joins
-// them with the prefix's sums, started early, took 47 and 250 us: it has the memory to
-// itself only when the products are done.)
+// own ones (68 MB) 37 us: 4 until a block has its line, 13 to 27 for its shares, 5 for
+// the join. (The own keys by a kernel at warp level that also joins
+// them with the prefix's sums, started early, took 252 and 47 us, this one then 234 and 41: it has the
+// memory to itself only when the products are done.)
 #include <algorithm>
 #include <type_traits>
 
