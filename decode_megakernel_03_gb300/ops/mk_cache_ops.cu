@@ -114,7 +114,7 @@ __device__ __forceinline__ void store(uint16_t* p, const float* x) {
 
 // ---- rotary positions and append ------------------------------------------------
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 128, kRopeRowThreads = 256;  // of a block; of one with a single row
 constexpr int kRopeTokens = 4;  // most tokens of a block
 
 struct RopeParams {
@@ -174,7 +174,7 @@ __device__ __forceinline__ void find_rows(const RopeParams& p, RopeRows<D>& s) {
     }
   }
   __syncthreads();
-  for (int i = tid; i < p.tokens * (D / 2); i += kRopeThreads) {
+  for (int i = tid; i < p.tokens * (D / 2); i += blockDim.x) {
     const int tok = i / (D / 2), pair = i % (D / 2);
     float2 v = make_float2(1.f, 0.f);  // behind rotary_dim: passes through
     if (2 * pair < p.rope.rotary_dim) {
@@ -201,19 +201,20 @@ __device__ __forceinline__ void find_rows(const RopeParams& p, RopeRows<D>& s) {
 // against 132 for the 32768 rows below in halves of 64, 450 against 138 in
 // halves of 62, where the partners were loaded one by one.)
 // Bound by the bytes of the rows: 32768 rows of the 8B shape, bf16, 805 MB, take
-// 125 us as neighbours, 6.4 TB/s; U heads of a lane are in flight: 133 us with 2,
-// 136 with 8. 200 rows take 4 to 5 us, a launch's latency.
+// 124 us as neighbours, 6.5 TB/s (blocks of 256 threads 125); U heads of a lane are in flight: 133 us with 2,
+// 136 with 8. 200 rows take 4 to 5 us, a launch's latency; a block of a single row has 256
+// threads there, with 128 it took 0.2 us more.
 template <typename T, int D, int PIECE>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int LPH = D / 8, HPW = 32 / LPH, WARPS = kRopeThreads / 32, U = 4;
+__global__ void __launch_bounds__(kRopeRowThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int LPH = D / 8, HPW = 32 / LPH, U = 4;
   __shared__ RopeRows<D> s;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row0 = blockIdx.x * p.tokens;
   find_rows<D>(p, s);
 
-  const int tok = warp % p.tokens;  // tokens divides WARPS
+  const int tok = warp % p.tokens;  // tokens divides warps
   if (s.pos[tok] < 0) return;
-  const int n_kv = p.cache.n_kv, heads = p.nh + 2 * n_kv, step = WARPS / p.tokens * HPW;
+  const int n_kv = p.cache.n_kv, heads = p.nh + 2 * n_kv, step = warps / p.tokens * HPW;
   const int c = lane % LPH, half = p.rope.rotary_dim / 2;
   const int64_t row = row0 + tok;
   const uint32_t crow = s.row[tok];
@@ -441,7 +442,7 @@ template <typename T, int D, int PIECE, bool NORM>
 void launch_rope(const RopeParams& p, cudaStream_t st) {
   const dim3 grid((p.rows + p.tokens - 1) / p.tokens);
   if constexpr (NORM) norm_rope_append_kernel<T, D, PIECE><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_append_kernel<T, D, PIECE><<<grid, kRopeThreads, 0, st>>>(p);
+  else rope_append_kernel<T, D, PIECE><<<grid, p.tokens == 1 ? kRopeRowThreads : kRopeThreads, 0, st>>>(p);
 }
 template <typename T, int D, bool NORM>
 void launch_rope(const RopeParams& p, cudaStream_t st) {
