@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kRopeRowThreads) rope_append_kernel(const __gr
 // that leaves fp32's range is taken again from x 2^-70. Only the result is rounded.
 // Bound by the bytes, with less room to wait for them than the rotation alone has: 32768 rows
 // of the 8B shape, bf16 in halves, 805 MB, take 131 us, 6.1 TB/s. Weights and rotation one
-// after another: 170; blocks of 256 threads: 142, and 153 with as many registers as it
-// would like; sixteen elements a lane: 155 to 171. 600 rows take 6 us, a launch's latency and
+// after another: 170. With one call to a graph, where this takes 133: blocks of 256 threads 144,
+// and 155 with as many registers as it would like; sixteen elements a lane 157 to 174. 600 rows take 6 us, a launch's latency and
 // that of a row's position, angle and queries.
 template <typename T, int D, int PIECE>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 7 : 4) norm_rope_append_kernel(const __grid_constant__ RopeParams p) {

@@ -294,7 +294,7 @@ __device__ __forceinline__ void over_values(int first, int hi, const R& rows, Ta
 // chains of 8, 132 MB of rows, take 52 us, 2.5 TB/s. Measured and slower: copies to shared
 // memory ahead of the sums, 16 bytes a thread each (4300 cycles for the 1900); two groups of
 // values at a time in the race or the residual's sum (registers; 59 us); 512 threads a block
-// (clusters of 16 that no longer fit all at once: 46 us for 8 sampled trees instead of 32).
+// (clusters of 16 that no longer fit all at once, it seems: 46 us for 8 sampled trees instead of 35).
 template <typename L, typename Q, bool VEC>
 __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ Shared sm;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
     // ---- the node's softmax, and its children
     row = (const L*)p.logits + (base + cur) * p.logits_stride;
     draft = (const Q*)p.draft + (base + cur) * p.draft_stride;
-    // (more than two rounds of loads: into the L2 cache at once, 7200 -> 5700 cycles)
+    // (more than two rounds of loads: into the L2 cache at once: 5300 to 5700 cycles, else 6900 to 7700)
     if (step > 0 && p.span > 16 / (int)sizeof(L) * kStride) fetch_part(row, sizeof(L));
     f.only = -1;
     f.top = -INFINITY;
