@@ -49,8 +49,8 @@ struct PrefixParams : AttnParams {
   int row_log2;                    // of row_tile
   uint32_t inv_G, inv_T;           // for div_by
   // The workspace: part_o, part_ml with two row tiles for each group of blocks (cut items), then
-  // every row twice (uncut items, of a prefix and own); for each sequence its plan; the line's
-  // length. A cut item's part_o holds eight columns of all rows of its tile and then the next
+  // every row twice (uncut items, of a prefix and own); the runs; for each sequence its plan; the
+  // line's length. A cut item's part_o holds eight columns of all rows of its tile and then the next
   // eight, so that neighbouring rows' threads store to neighbouring places (row after row 128
   // rows took 5900 cycles) and the join's lanes read whole sectors.
   int64_t cut_rows;
@@ -458,8 +458,11 @@ constexpr char kName[] = "mk_prefix_attention";
 struct PrefixPlan {
   int row_tile, groups;
   int64_t cut_rows, rows;  // rows of the workspace: of cut items, all
+  size_t runs;             // float4
   size_t sums(int D) const { return ((size_t)rows * (D + 2) * sizeof(float) + 31) / 32 * 32; }
-  size_t bytes(int D, int B) const { return sums(D) + (size_t)B * sizeof(RowPlan) + sizeof(int); }
+  size_t bytes(int D, int B) const {
+    return sums(D) + runs * sizeof(float4) + (size_t)B * sizeof(RowPlan) + sizeof(int);
+  }
 };
 
 // The row tile by the rows of a group, were all alike.
@@ -492,15 +495,17 @@ int check_prefix(const mk_cache* cache, int batch, int n_tokens, int n_heads, in
   return MK_OK;
 }
 
-int make_plan(int B, int T, int nh, int G, int type, int n_groups, PrefixPlan* pl) {
+int make_plan(const CacheView& cache, int D, int B, int T, int nh, int type, int n_groups,
+              PrefixPlan* pl) {
   int device = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return op_cuda(e, kName);
-  pl->row_tile = row_tile_of(B, T, G, type, n_groups);
+  pl->row_tile = row_tile_of(B, T, nh / cache.n_kv, type, n_groups);
   pl->groups = n_sm;
   pl->cut_rows = (int64_t)2 * pl->groups * pl->row_tile;
   pl->rows = pl->cut_rows + 2 * (int64_t)B * T * nh;
+  pl->runs = run_vectors(type, pl->row_tile, ((int64_t)cache.capacity + kKeys - 1) / kKeys, pl->groups, D);
   return MK_OK;
 }
 
@@ -535,8 +540,7 @@ int mk_prefix_attention_workspace(const mk_cache* cache, int batch, int n_tokens
   CacheView view;
   PrefixPlan pl;
   if (int rc = check_prefix(cache, batch, n_tokens, n_heads, type, n_groups, &view)) return rc;
-  if (int rc = make_plan(batch, n_tokens, n_heads, n_heads / cache->n_kv_heads, type, n_groups, &pl))
-    return rc;
+  if (int rc = make_plan(view, cache->head_dim, batch, n_tokens, n_heads, type, n_groups, &pl)) return rc;
   *bytes = pl.bytes(cache->head_dim, batch);
   return MK_OK;
 }
@@ -562,8 +566,7 @@ int mk_prefix_attention(const mk_cache* cache, int layer, int batch, int n_token
     return op_fail(MK_ERR_INVALID,
                    "q, out: 16-byte aligned rows, strides at least a row, are needed");
   if (!aligned(workspace, 256)) return op_fail(MK_ERR_INVALID, "workspace: not 256-byte aligned");
-  if (int rc = make_plan(batch, n_tokens, n_heads, n_heads / cache->n_kv_heads, type, n_groups, &pl))
-    return rc;
+  if (int rc = make_plan(p.cache, cache->head_dim, batch, n_tokens, n_heads, type, n_groups, &pl)) return rc;
   if (workspace_bytes < pl.bytes(cache->head_dim, batch))
     return op_fail(MK_ERR_INVALID, "workspace: smaller than its query says");
   p.k = (const uint16_t*)cache->k[layer];
@@ -585,7 +588,9 @@ int mk_prefix_attention(const mk_cache* cache, int layer, int batch, int n_token
   p.cut_rows = pl.cut_rows;
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + (size_t)pl.rows * cache->head_dim;
-  p.plans = (RowPlan*)((uint8_t*)workspace + pl.sums(cache->head_dim));
+  float4* runs = (float4*)((uint8_t*)workspace + pl.sums(cache->head_dim));
+  p.runs = pl.runs ? runs : nullptr;
+  p.plans = (RowPlan*)(runs + pl.runs);
   p.length = (int*)(p.plans + batch);
   auto inverse = [](int d) { return (uint32_t)std::min<uint64_t>((1ull << 32) / d + 1, UINT32_MAX); };
   p.inv_G = inverse(p.G), p.inv_T = inverse(p.T);

@@ -554,7 +554,8 @@ __global__ void __launch_bounds__(128) tree_attention_join(const __grid_constant
 struct Plan {
   bool tc;  // the kernel for many rows
   int tile, extra, row_tile, row_tiles, groups;
-  size_t o_floats, ml_floats;
+  size_t o_floats, ml_floats, runs;  // runs: float4
+  size_t bytes() const { return (o_floats + ml_floats) * sizeof(float) + runs * sizeof(float4); }
 };
 
 // Which kernel, and its tiles. Up to 16 rows go to the warp-level kernel, whose
@@ -581,7 +582,7 @@ struct Plan {
 // 170, over 32768 285 / 315 against 308 / 325, over 4096 59 / 68 against 62 / 65; the
 // lengths are not known here, and one sequence over 2048 keys, where the second
 // block's share only adds to the first's, takes 27 / 30 us against 23 / 24.
-Plan plan_of(int T, int G, int D, int type, int n_sm) {
+Plan plan_of(const CacheView& cache, int B, int T, int G, int D, int type, int n_sm) {
   Plan pl;
   const int rows = T * G;
   pl.tc = rows > kRows || (type == MK_TYPE_FP32 && D == 128);
@@ -610,6 +611,9 @@ Plan plan_of(int T, int G, int D, int type, int n_sm) {
   const size_t slots = (size_t)pl.groups * 2 * pl.row_tiles * pl.row_tile;
   pl.o_floats = slots * D;
   pl.ml_floats = slots * 2;
+  // a share has no more tiles than a context, or than a block's part of the longest line
+  const int64_t tiles = ((int64_t)cache.capacity + 127) / 128, line = (int64_t)B * cache.n_kv * (tiles + pl.extra);
+  pl.runs = pl.tc ? run_vectors(type, pl.row_tile, std::min(tiles, line / pl.groups + 1), pl.groups * pl.row_tiles, D) : 0;
   return pl;
 }
 
@@ -630,12 +634,12 @@ int check_attention(const mk_cache* cache, int batch, int n_tokens, int n_heads,
   return MK_OK;
 }
 
-int make_plan(const mk_cache* cache, int n_tokens, int n_heads, int type, Plan* pl) {
+int make_plan(const CacheView& view, int D, int batch, int n_tokens, int n_heads, int type, Plan* pl) {
   int device = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return op_cuda(e, "mk_tree_attention");
-  *pl = plan_of(n_tokens, n_heads / cache->n_kv_heads, cache->head_dim, type, n_sm);
+  *pl = plan_of(view, batch, n_tokens, n_heads / view.n_kv, D, type, n_sm);
   return MK_OK;
 }
 
@@ -688,8 +692,8 @@ int mk_tree_attention_workspace(const mk_cache* cache, int batch, int n_tokens, 
   CacheView view;
   Plan pl;
   if (int rc = check_attention(cache, batch, n_tokens, n_heads, type, &view)) return rc;
-  if (int rc = make_plan(cache, n_tokens, n_heads, type, &pl)) return rc;
-  *bytes = (pl.o_floats + pl.ml_floats) * sizeof(float);
+  if (int rc = make_plan(view, cache->head_dim, batch, n_tokens, n_heads, type, &pl)) return rc;
+  *bytes = pl.bytes();
   return MK_OK;
 }
 
@@ -714,8 +718,8 @@ int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens,
     return op_fail(MK_ERR_INVALID,
                    "q, out: 16-byte aligned rows, strides at least a row, are needed");
   if (!aligned(workspace, 256)) return op_fail(MK_ERR_INVALID, "workspace: not 256-byte aligned");
-  if (int rc = make_plan(cache, n_tokens, n_heads, type, &pl)) return rc;
-  if (workspace_bytes < (pl.o_floats + pl.ml_floats) * sizeof(float))
+  if (int rc = make_plan(p.cache, cache->head_dim, batch, n_tokens, n_heads, type, &pl)) return rc;
+  if (workspace_bytes < pl.bytes())
     return op_fail(MK_ERR_INVALID, "workspace: smaller than its query says");
   p.k = (const uint16_t*)cache->k[layer];
   p.v = (const uint16_t*)cache->v[layer];
@@ -728,6 +732,7 @@ int mk_tree_attention(const mk_cache* cache, int layer, int batch, int n_tokens,
   p.scale_log2 = scale * 1.4426950408889634f;
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + pl.o_floats;
+  p.runs = pl.runs ? (float4*)(p.part_ml + pl.ml_floats) : nullptr;
   cudaStream_t st = (cudaStream_t)stream;
   return cache->head_dim == 64 ? launch_all<64>(p, pl, type, st) : launch_all<128>(p, pl, type, st);
 }

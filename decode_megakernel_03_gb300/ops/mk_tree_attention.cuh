@@ -44,7 +44,28 @@ struct AttnParams {
   float scale_log2;            // scale * log2(e)
   float* part_o;               // [groups][2][row_tiles][row_tile][D]
   float* part_ml;              // [groups][2][row_tiles][row_tile][2]: (max, sum)
+  float4* runs;                // run_vectors of them; nullptr: no share has more than one run
 };
+
+// Tiles that a stream of bf16 rows of the tensor-memory kernel sums up there at most. The unit
+// truncates as it accumulates, always towards zero, a product of 16 keys by up to 2^-22 of the
+// sum before it: where all values have one sign a sum over 2^20 keys in one run lost 2^-7 of
+// itself, five roundings of the output. So after a run of kRun tiles (16 products each: 2^-13 at
+// worst) the rows' threads add what is in tensor memory to the sums of the runs before, in the
+// workspace and rounded, and the next tile begins a new one. Only the kernels for caches that may
+// hold so many keys have the code for it (RUNS), which costs by being there. Runs of 32 tiles, of
+// 64 (2^-12), and without (8B shape): 8 x 64 nodes over 16384 to 32768 keys 240, 235, 231 us; 4 x 8
+// nodes over 131072 keys 320, 310, 307; 64 samples of two documents (mk_prefix_attention.cu) 222,
+// 222, 211, and 222 with 128, where no run ends.
+constexpr int kRun = 32;
+
+// The room for the earlier runs' sums: for each block and its two streams four columns of 128
+// rows and then the next four. None where no share can have more than a run: `most` tiles, which
+// a single block of rows takes in two streams.
+inline size_t run_vectors(int type, int row_tile, int64_t most, int blocks, int D) {
+  const bool runs = type == MK_TYPE_BF16 && most > (row_tile > 128 ? kRun : 2 * kRun);
+  return runs ? (size_t)blocks * 2 * (D / 4) * 128 : 0;
+}
 
 // ---- the line of work -----------------------------------------------------------
 // Sequence b has nt(b) tiles for each kv-head; items are ordered (b, g), each is

@@ -240,6 +240,7 @@ struct Shared {
   uint32_t odd[2];
   uint32_t odd_at[2][MK_MAX_TREE][2][4];
   float ml[128][2];                // kOne: stream 1's (m, l)
+  float run_m[2][128];             // RUNS: the reference of a stream's earlier runs
   // fp32: a tile's product is in tensor memory / has been read; the halves'
   // maxima (by tile parity) and sums
   uint64_t t_full[2], t_free[2];
@@ -405,7 +406,7 @@ __device__ __forceinline__ void load_role(const P& p, Shared& sm, const typename
 // Products run in the order of their issue, so the scores of a stream's next tile
 // may be issued over the weights that its last products read.
 
-template <int D, int KIND, class P>
+template <int D, int KIND, bool RUNS, class P>
 __device__ __forceinline__ void mma_role(const P& p, Shared& sm, const typename P::Line& line,
                                          uint32_t q_smem, uint32_t ring, uint32_t tmem, int u_begin,
                                          int u_end, int rt) {
@@ -419,6 +420,8 @@ __device__ __forceinline__ void mma_role(const P& p, Shared& sm, const typename 
   typename P::Share sh;
   // S of stream s from the K tile in buffer `at`; free: it is not needed again
   bool two = false;  // of the share
+  // whether tile `i` of a stream adds to what is in tensor memory
+  auto goes_on = [](int i) { return RUNS ? i % kRun != 0 : i > 0; };
   auto scores = [&](int s, uint32_t at, bool free) {
     if (elect_one()) {
       const uint64_t k = operand(ring + at * Lay::kBuf, 16);
@@ -491,7 +494,7 @@ __device__ __forceinline__ void mma_role(const P& p, Shared& sm, const typename 
         const int s = i & 1;
         if (i >= 0) {
           if (s == 0) v_at = take();
-          values(s, v_at, i >= 2, s == 1);
+          values(s, v_at, goes_on(i / 2), s == 1);
           if (s == 0 && i + 2 < 2 * sh.n) k_at = take();
         }
         if (i + 2 < 2 * sh.n) scores(s, k_at, s == 1);
@@ -500,7 +503,7 @@ __device__ __forceinline__ void mma_role(const P& p, Shared& sm, const typename 
       for (int s = 0; s < 2 && s < sh.n; ++s) scores(s, take(), true);
       for (int j = 0; j < sh.n; ++j) {
         const int s = j & 1;
-        values(s, take(), !Lay::EXACT && j >= 2, true);
+        values(s, take(), !Lay::EXACT && goes_on(j / 2), true);
         if (j + 2 < sh.n) scores(s, take(), true);
       }
     }
@@ -782,7 +785,7 @@ __device__ __forceinline__ bool wait_failed(Shared& sm) {
 }
 
 // kOne, kTwo: softmax of a stream.
-template <int D, int KIND, class P>
+template <int D, int KIND, bool RUNS, class P>
 __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typename P::Line& line,
                                              uint8_t* q_ptr, uint32_t tmem, int u_begin,
                                              int u_end, int rt, int group) {
@@ -793,6 +796,37 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
   const uint32_t t_s = tmem + lanes + stream * Lay::kScoreStep;
   const uint32_t t_o = tmem + lanes + Lay::kOut + stream * D;
   const unsigned long long scale2 = pack2(p.scale_log2, p.scale_log2);
+  // What is in tensor memory and the sums of the runs before it (some), added up relative to
+  // m: to where those are (keep) or to tensor memory.
+  auto end_run = [&](float m, bool some, bool keep) {
+    const float from = some ? sm.run_m[stream][r] : m, back = from == m ? 1.f : fast_exp2(from - m);
+    if (keep) sm.run_m[stream][r] = m;
+    float4* runs = p.runs + ((size_t)blockIdx.x * 2 + stream) * (D / 4) * 128 + r;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      uint32_t o[32];
+      tmem_load32(t_o + c, o);
+      tmem_wait_ld<32>(o);
+#pragma unroll
+      for (int e = 0; e < 32; e += 4, runs += 128) {
+        float4 y = {};
+        if (some) y = *runs;
+        y.x = fmaf(y.x, back, __uint_as_float(o[e]));
+        y.y = fmaf(y.y, back, __uint_as_float(o[e + 1]));
+        y.z = fmaf(y.z, back, __uint_as_float(o[e + 2]));
+        y.w = fmaf(y.w, back, __uint_as_float(o[e + 3]));
+        if (keep) {
+          *runs = y;
+        } else {
+          o[e] = __float_as_uint(y.x), o[e + 1] = __float_as_uint(y.y);
+          o[e + 2] = __float_as_uint(y.z), o[e + 3] = __float_as_uint(y.w);
+        }
+      }
+      if (!keep) tmem_store32(t_o + c, o);
+    }
+    if (!keep) tmem_wait_st();
+    __syncwarp();
+  };
   Waiter wait(sm);
   uint32_t s_uses = 0, tile_no = 0;
   int u = u_begin;
@@ -817,13 +851,19 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
     for (int j = two ? 0 : stream; j < sh.n; j += two ? 1 : 2) {
       wait(&sm.s_full[stream], s_uses++);
       tc_fence_after();
+      bool run_ends = false;  // before this tile
+      if constexpr (RUNS) {
+        const int i = two ? j : j / 2;  // the stream's tiles before this one
+        run_ends = i > 0 && i % kRun == 0;
+        if (run_ends && warp_live) end_run(m, i > kRun, true);
+      }
       if (warp_live) {
         uint32_t x[kKeys];
         const Sight v = sight_of(sm.mask[(tile_no + j) % kMasks], sh.start - first_slot(sh) - (sh.k0 + j) * kKeys, seen);
         const float top = read_scores(t_s, v.some, v.bits, x);
         const float keep = move_reference(top * p.scale_log2, m, l);
         const int before = two ? j : j / 2;  // tiles already in O
-        if (before > 0 && __any_sync(0xffffffffu, keep != 1.f)) {
+        if (before > 0 && !run_ends && __any_sync(0xffffffffu, keep != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -876,7 +916,12 @@ __device__ __forceinline__ void softmax_role(const P& p, Shared& sm, const typen
     }
     wait(&sm.o_full, share);
     tc_fence_after();
+    if (RUNS && (two ? sh.n : (sh.n + 1 - stream) / 2) > kRun && warp_live) {
+      end_run(m, true, false);
+      tc_fence_before();
+    }
     if (!two) named_bar(1, 32 * kSoftWarps);
+    if (RUNS && !two) tc_fence_after();
     if ((two || stream == 0) && warp_live) {
       float f0 = 1.f, f1 = 0.f;  // factors of the streams' shares (one row block)
       if (!two) {
@@ -1067,7 +1112,7 @@ __device__ __forceinline__ void exact_role(const P& p, Shared& sm, const typenam
   }
 }
 
-template <int D, int KIND, class P>
+template <int D, int KIND, bool RUNS, class P>
 __global__ void __launch_bounds__(kThreads, 1)
 tree_attention_tc_kernel(const __grid_constant__ P p) {
   using Lay = Layout<D, KIND>;
@@ -1119,7 +1164,7 @@ tree_attention_tc_kernel(const __grid_constant__ P p) {
     if constexpr (Lay::EXACT) {
       exact_role<D, KIND, P>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
     } else {
-      softmax_role<D, KIND, P>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
+      softmax_role<D, KIND, RUNS, P>(p, sm, line, base, tmem, u_begin, u_end, rt, group);
     }
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -1128,7 +1173,7 @@ tree_attention_tc_kernel(const __grid_constant__ P p) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kMmaWarp + 1) put_plans(p, line);
     if (warp == kMmaWarp)
-      mma_role<D, KIND, P>(p, sm, line, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
+      mma_role<D, KIND, RUNS, P>(p, sm, line, smem_u32(base), smem_u32(ring_ptr), tmem, u_begin, u_end, rt);
   }
   tc_fence_before();
   __syncthreads();
@@ -1136,14 +1181,21 @@ tree_attention_tc_kernel(const __grid_constant__ P p) {
   if (warp == kMmaWarp) tmem_free(tmem, 512);
 }
 
-template <int D, int KIND, class P>
-int launch_kind(const P& p, int blocks, const char* name, cudaStream_t st) {
+template <int D, int KIND, bool RUNS, class P>
+int launch_kernel(const P& p, int blocks, const char* name, cudaStream_t st) {
   using Lay = Layout<D, KIND>;
-  auto* fn = tree_attention_tc_kernel<D, KIND, P>;
+  auto* fn = tree_attention_tc_kernel<D, KIND, RUNS, P>;
   static std::atomic<uint64_t> ready{0};
   if (int rc = allow_shared(ready, (const void*)fn, Lay::kBytes, name)) return rc;
   fn<<<blocks, kThreads, Lay::kBytes, st>>>(p);
   return op_cuda(cudaGetLastError(), name);
+}
+
+template <int D, int KIND, class P>
+int launch_kind(const P& p, int blocks, const char* name, cudaStream_t st) {
+  if constexpr (!Layout<D, KIND>::EXACT)
+    if (p.runs) return launch_kernel<D, KIND, true>(p, blocks, name, st);
+  return launch_kernel<D, KIND, false>(p, blocks, name, st);
 }
 
 // The kind by the row tile: fp32 32 or 128 rows, bf16 up to 128 or 256.

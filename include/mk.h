@@ -453,7 +453,8 @@ int mk_norm_rope_append(const mk_rope* rope, const void* q_norm, const void* k_n
    ([n_heads][head_dim]); n_heads a multiple of n_kv_heads, at most 8 query
    heads per kv-head; n_tokens 1 to MK_MAX_TREE. Softmax of scale * (q . k) in
    fp32; its weights enter the product with the values as bf16 parts that hold them
-   to 2^-16 (fp32 calls: weights and queries to 2^-24). A row that sees no key is 0;
+   to 2^-16 (fp32 calls: weights and queries to 2^-24); a bf16 call's sums lose at most 2^-13
+   of themselves, however long the context, as the matrix unit truncates. A row that sees no key is 0;
    NaN and infinities in rows it does not see do not reach it. Infinities that it does
    see in keys or in the context's values may make it NaN where the formula gives
    an infinity or a weight of 0. out may be q (with q's stride). Deterministic: the same
