@@ -41,10 +41,18 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], uint32_t addr) {
 // latency: 512 keys of one sequence 9.2 us, two launches of which the second
 // waits for the first inside.
 constexpr int tile_keys(int D) { return 8192 / D; }
+// How the weights times the values are added up, as the matrix unit truncates when it
+// accumulates (kRun): in heads of 64 and in fp32 by rounded adds of each product; in bf16 heads of
+// 128 in the unit, and the sums of so many tiles to the workspace (a warp takes a quarter of a
+// tile's keys, so that these are as many products as a run of the other kernel). 8 tokens over
+// 16384 keys each, 8B shape: 84.1 us with runs, 83.9 without, 90.3 with rounded adds, which spill
+// there; 4 tokens over 131072 keys, 1B shape: 160.9 with rounded adds, 159.3 without, 166.6 with runs.
+constexpr int run_tiles(int D) { return 4 * kRun * 128 / tile_keys(D); }
 
 template <int D, int P>
 struct Layout {
-  static constexpr int kTile = tile_keys(D);
+  static constexpr int kTile = tile_keys(D), kRunTiles = run_tiles(D);
+  static constexpr bool kRuns = P == 1 && D == 128;
   static constexpr int kStageBytes = 2 * kTile * D * 2;
   static constexpr int kRing = kStages * kStageBytes;
   // joined warps: o [4][kRows][D] fp32 over the ring
@@ -69,6 +77,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
   // [0], -inf in [1], NaN in both
   __shared__ uint32_t s_odd[MK_MAX_TREE][2][D / 32];
   __shared__ float s_ml[4][RT][2];
+  __shared__ float s_run[kThreads][2];  // the reference of the thread's earlier runs
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int grp = lane / 4, tig = lane % 4;
   const int rt = blockIdx.x % p.row_tiles, group = blockIdx.x / p.row_tiles;
@@ -201,8 +210,34 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
     mx[0] = mx[1] = -INFINITY;
     sum[0] = sum[1] = 0.f;
 
+    // adds the sums of the runs before this one (some) to o
+    auto add_runs = [&](const float4* runs) {
+      float back[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float from = s_run[tid][h];
+        back[h] = from == mx[h] ? 1.f : fast_exp2(from - mx[h]);
+      }
+#pragma unroll
+      for (int d = 0; d < NB; ++d) {
+        const float4 x = runs[d * kThreads];
+        o[d][0] = fmaf(x.x, back[0], o[d][0]), o[d][1] = fmaf(x.y, back[0], o[d][1]);
+        o[d][2] = fmaf(x.z, back[1], o[d][2]), o[d][3] = fmaf(x.w, back[1], o[d][3]);
+      }
+    };
+    float4* runs = p.runs + (size_t)blockIdx.x * NB * kThreads + tid;
+
     // ---- the tiles
     for (int it = 0; it < n; ++it) {
+      if (Lay::kRuns && it % Lay::kRunTiles == 0 && it > 0) {  // a run ends
+        if (it > Lay::kRunTiles) add_runs(runs);
+#pragma unroll
+        for (int d = 0; d < NB; ++d) {
+          runs[d * kThreads] = make_float4(o[d][0], o[d][1], o[d][2], o[d][3]);
+          o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
+        }
+        s_run[tid][0] = mx[0], s_run[tid][1] = mx[1];
+      }
       cp_async_wait<kStages - 2>();
       __syncthreads();  // tile `it` is there; everybody is done with tile it - 1
       fetch(it + kStages - 1);
@@ -341,7 +376,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
           const int r = (warp * NK + nk) * 16 + (lane / 8) % 2 * 8 + lane % 8, c = d + lane / 16;
           uint32_t vf[4];
           ldsm_x4_t(vf, vs + r * (D * 2) + ((c ^ (r & 7)) * 16));
-          if constexpr (P == 1) {
+          if constexpr (Lay::kRuns) {
 #pragma unroll
             for (int q = W - 1; q >= 0; --q) {
               mma_bf16_16816(o[d], w[q], vf[0], vf[1]);
@@ -350,7 +385,7 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
           } else {
             float x[2][4] = {};
 #pragma unroll
-            for (int q = P - 1; q >= 0; --q) {
+            for (int q = W - 1; q >= 0; --q) {
               mma_bf16_16816(x[0], w[q], vf[0], vf[1]);
               mma_bf16_16816(x[1], w[q], vf[2], vf[3]);
             }
@@ -377,6 +412,8 @@ tree_attention_kernel(const __grid_constant__ AttnParams p) {
       }
       if (tid < kTile) rowtab[(it + kStages) % (kStages + 1) * kTile + tid] = next_row;
     }
+
+    if (Lay::kRuns && n > Lay::kRunTiles) add_runs(runs);
 
     // ---- the warps' shares joined: sums within a quad, maxima across warps
     cp_async_wait<0>();
@@ -612,8 +649,10 @@ Plan plan_of(const CacheView& cache, int B, int T, int G, int D, int type, int n
   pl.o_floats = slots * D;
   pl.ml_floats = slots * 2;
   // a share has no more tiles than a context, or than a block's part of the longest line
-  const int64_t tiles = ((int64_t)cache.capacity + 127) / 128, line = (int64_t)B * cache.n_kv * (tiles + pl.extra);
-  pl.runs = pl.tc ? run_vectors(type, pl.row_tile, std::min(tiles, line / pl.groups + 1), pl.groups * pl.row_tiles, D) : 0;
+  const int64_t tiles = ((int64_t)cache.capacity + pl.tile - 1) / pl.tile, line = (int64_t)B * cache.n_kv * (tiles + pl.extra);
+  const int64_t most = std::min(tiles, line / pl.groups + 1);
+  if (pl.tc) pl.runs = run_vectors(type, pl.row_tile, most, pl.groups * pl.row_tiles, D);
+  else pl.runs = D == 128 && most > run_tiles(D) ? (size_t)pl.groups * pl.row_tiles * (D / 8) * kThreads : 0;
   return pl;
 }
 

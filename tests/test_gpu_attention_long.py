@@ -53,10 +53,11 @@ def case(op, keys, T, nh, D, mean):
     return torch.stack(got), torch.stack(want)
 
 
-# rows of a kv-head pick the kernel: 32 one block of rows, 256 two; for a prefix the rows of all 19
-# sequences, 38, 152 and more
-SHAPES = [("tree", 4, 64, 128), ("tree", 4, 64, 64), ("tree", 32, 64, 128), ("tree", 32, 64, 64), ("prefix", 1, 16, 128),
-          ("prefix", 1, 64, 128), ("prefix", 1, 64, 64), ("prefix", 4, 64, 128)]
+# rows of a kv-head pick the kernel: 2, 8 and 16 the one for few rows, 32 one block of rows, 256 two; for
+# a prefix the rows of all 19 sequences, 38, 152 and more
+SHAPES = [("tree", 1, 16, 128), ("tree", 1, 64, 64), ("tree", 2, 64, 128), ("tree", 4, 64, 128), ("tree", 4, 64, 64),
+          ("tree", 32, 64, 128), ("tree", 32, 64, 64), ("prefix", 1, 16, 128), ("prefix", 1, 64, 128),
+          ("prefix", 1, 64, 64), ("prefix", 4, 64, 128)]
 
 
 @pytest.mark.parametrize("op,T,nh,D", SHAPES)
@@ -71,11 +72,13 @@ def test_loss_does_not_grow(keys, op, T, nh, D):
 
 
 @pytest.mark.parametrize("way", ["rising", "falling", "first pages missing"])
-@pytest.mark.parametrize("op,T,D", [("tree", 4, 128), ("tree", 32, 64), ("tree", 32, 128), ("prefix", 4, 128), ("prefix", 4, 64)])
+@pytest.mark.parametrize("op,T,D", [("tree", 2, 128), ("tree", 4, 128), ("tree", 32, 64), ("tree", 32, 128), ("prefix", 4, 128),
+                                    ("prefix", 4, 64)])
 def test_reference_moves(op, T, D, way):
     """Scores that grow along the context (each part's largest is far above the last one's), fall, or begin
     behind the first 70 tiles."""
     keys, nh = 24576 - 64, 64
+    seqs = 2 * B if T == 2 else B  # (the kernel for few rows has two blocks per SM)
     g = torch.Generator(device="cuda").manual_seed(T + D)
     new = lambda *s: torch.randn(s, generator=g, device="cuda")
     n = (keys + 64) // PAGE
@@ -86,12 +89,12 @@ def test_reference_moves(op, T, D, way):
         size[:] = 1
     k = (new(n, NKV, PAGE, D) * size.view(n, 1, PAGE, 1)).bfloat16()
     v = (new(n, NKV, PAGE, D) + 0.5).bfloat16()
-    q = new(B, T, nh, D).bfloat16()
+    q = new(seqs, T, nh, D).bfloat16()
     ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
     table = torch.arange(n, device="cuda", dtype=torch.int32)
     gone = 70 * 128 // PAGE if way == "first pages missing" else 0
     table[:gone] = -1
-    cache, starts, roots = mk.Cache([k], [v], table.expand(B, n).contiguous()), ints([keys] * B), ints([[-1] * T] * B)
+    cache, starts, roots = mk.Cache([k], [v], table.expand(seqs, n).contiguous()), ints([keys] * seqs), ints([[-1] * T] * seqs)
     if op == "tree":
         out = mk.tree_attention(cache, 0, q, starts, roots)
     else:  # (the sequences' own keys are the long part)
@@ -100,7 +103,7 @@ def test_reference_moves(op, T, D, way):
     kk, vv = flat(k), flat(v)
     at, t = torch.arange(keys + 64, device="cuda"), torch.arange(T, device="cuda")
     seen = ((at < keys) & (at >= gone * PAGE)) | (at == keys + t[:, None])
-    for b in (0, B - 1):
+    for b in (0, seqs - 1):
         qq = q[b].reshape(T, NKV, nh // NKV, D).permute(1, 0, 2, 3).double()
         s = torch.einsum("htgd,hkd->htgk", qq, kk) * D**-0.5
         w = torch.softmax(s.masked_fill(~seen[None, :, None], float("-inf")), -1)
