@@ -201,9 +201,9 @@ __device__ __forceinline__ void find_rows(const RopeParams& p, RopeRows<D>& s) {
 // against 132 for the 32768 rows below in halves of 64, 450 against 138 in
 // halves of 62, where the partners were loaded one by one.)
 // Bound by the bytes of the rows: 32768 rows of the 8B shape, bf16, 805 MB, take
-// 124 us as neighbours, 6.5 TB/s (blocks of 256 threads 125); U heads of a lane are in flight: 133 us with 2,
-// 136 with 8. 200 rows take 4 to 5 us, a launch's latency; a block of a single row has 256
-// threads there, with 128 it took 0.2 us more.
+// 120 us as halves, 6.7 TB/s; U heads of a lane are in flight: 133 us with 2,
+// 136 with 8 (neighbours, four rows in 256 threads, where 4 took 125). 200 rows take 4 to 5 us, a
+// launch's latency; a block of a single row has 256 threads there, with 128 it took 0.2 us more.
 template <typename T, int D, int PIECE>
 __global__ void __launch_bounds__(kRopeRowThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPH = D / 8, HPW = 32 / LPH, U = 4;
@@ -494,11 +494,26 @@ int rope_append(RopeParams& p, const char* name, const mk_rope* rope, const mk_c
   p.qs = q_stride, p.ks = k_stride, p.vs = v_stride, p.os = q_out_stride;
   p.starts = starts, p.parents = parents, p.counts = counts;
   p.rows = batch * n_tokens, p.T = n_tokens, p.nh = n_heads;
-  // Rows of a block: one where the blocks are few (8B shape, bf16, 512 rows: 6.2 us
-  // against 7.2 with four), four where there are enough, since a block's rows
-  // then find their angles together (1024 rows 7.2 us against 8.2 with one, 2048
-  // 11.0 against 14.1, 32768 126 against 168).
-  p.tokens = p.rows >= 1024 ? kRopeTokens : 1;
+  // Rows of a block: one where the blocks are few (256 threads), from 1024 rows on two (128
+  // threads), since a block's rows then find their angles together, from 4096 on four where a
+  // row's heads are less than 8 KB. us for one, two, four rows, and four in 256 threads:
+  //   8B shape, bf16 (12 KB)   512 rows   4.6    5.7    8.6    5.9
+  //                           1024        6.7    6.4    9.2    6.6
+  //                           2048       13.0   10.9   13.7   11.1
+  //                           4096       23.1   19.1   19.5   20.4
+  //                          32768        159  119.9  124.4  127.3
+  //   1B shape, bf16 (6 KB)   1024        5.6    4.7    5.7    4.8
+  //                           2048        9.3    5.8    6.6    6.2
+  //                           4096       18.0   11.8   10.9   12.4
+  //                          32768        128   67.6   63.2   74.0
+  //   10 heads, fp32 (5 KB)   1024        6.4    3.9    4.6    4.0
+  //                           4096       19.7    9.8    9.9   11.1
+  //                          32768        138   52.6   52.0   59.8
+  //   8B shape, fp32 (24 KB)  4096       32.0   31.6   33.7   31.9
+  //                          32768        225  213.8  217.2  213.7
+  const int64_t row_bytes = (int64_t)(n_heads + 2 * cache->n_kv_heads) * cache->head_dim * (type == MK_TYPE_FP32 ? 4 : 2);
+  if (NORM) p.tokens = p.rows >= 1024 ? kRopeTokens : 1;
+  else p.tokens = p.rows < 1024 ? 1 : p.rows >= 4096 && row_bytes < 8192 ? kRopeTokens : 2;
   cudaStream_t st = (cudaStream_t)stream;
   if (type == MK_TYPE_FP32) {
     if (cache->head_dim == 64) launch_rope<float, 64, NORM>(p, st);

@@ -199,3 +199,38 @@ def test_binding_refusals():
         assert e.value.code == mk.MK_ERR_INVALID, i
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(k + v, before))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("nh,nkv,D", [(32, 8, 128), (7, 1, 64)])
+def test_rows_of_a_block(nh, nkv, D, norm, dtype):
+    """Blocks take one, two or four rows by the call's size (1023 to 4097 rows, heads above and below 8 KB a row): a
+    row's values do not depend on it."""
+    B, T = 3, 1366
+    starts, counts = [5, 0, 40], [1366, 1001, 3]
+    qkv = (torch.randn((B, T, nh + 2 * nkv, D), device=dev(), generator=torch.Generator(dev()).manual_seed(nh))).to(dtype)
+    w = [torch.linspace(0.5, 2, D, device=dev()).to(BF16) for _ in range(2)]
+    rope = mk.Rope(D, theta=500000.0)
+
+    def run(parts):
+        """(queries, k, v) by calls over runs of the sequences' rows"""
+        k, v = ([torch.zeros((B, nkv, 1500, D), dtype=BF16, device=dev())] for _ in range(2))
+        out = torch.full((B, T, nh, D), 77.0, device=dev(), dtype=dtype)
+        cache = mk.Cache(k, v)
+        for a, b in zip(parts, parts[1:]):
+            x = qkv[:, a:b].contiguous()
+            q, kn, vn = x.split([nh, nkv, nkv], 2)
+            left = [min(max(c - a, 0), b - a) for c in counts]
+            o = torch.full((B, b - a, nh, D), 77.0, device=dev(), dtype=dtype)
+            rest = (ints([s + a for s in starts]), None, ints(left))
+            if norm:
+                mk.norm_rope_append(rope, cache, 0, q, kn, vn, *w, *rest, q_out=o)
+            else:
+                mk.rope_append(rope, cache, 0, q, kn, vn, *rest, q_out=o)
+            out[:, a:b] = o
+        return out, k[0], v[0]
+
+    want = run(list(range(0, T, 341)) + [T])  # 1023 rows a call, 6 the last
+    for parts in ([0, T], [0, 1365, T], [0, 342, 1024, T], [0, 683, T]):  # 4098 rows, 4095, 1026, 2046, 2049
+        assert all(torch.equal(x, y) for x, y in zip(run(parts), want)), parts
