@@ -511,9 +511,25 @@ int rope_append(RopeParams& p, const char* name, const mk_rope* rope, const mk_c
   //                          32768        138   52.6   52.0   59.8
   //   8B shape, fp32 (24 KB)  4096       32.0   31.6   33.7   31.9
   //                          32768        225  213.8  217.2  213.7
+  // Normed, always 128 threads, two rows as long as all blocks are resident (7 per SM in bf16, 4
+  // in fp32), then four up to 16 KB:
+  //   8B shape, bf16 (12 KB)   512 rows   4.9    5.7    8.3
+  //                           1024        6.2    6.7    9.1
+  //                           2048       12.0   10.7   13.8
+  //                           4096       21.6   19.5   19.3
+  //                          32768        144  129.7  127.7
+  //   1B shape, bf16 (6 KB)   2048        7.8    6.1    6.7
+  //                           2560       10.5    8.5    7.7
+  //                           4096       15.7   12.2   10.8
+  //   10 heads, fp32 (5 KB)   1024        6.3    4.5    4.9
+  //                           1536        8.2    6.7    5.3
+  //   8B shape, fp32 (24 KB)  2048       17.4   17.7   17.7
+  //                           4096       32.3   30.8   33.7
+  //                          32768        221  212.5  215.3
   const int64_t row_bytes = (int64_t)(n_heads + 2 * cache->n_kv_heads) * cache->head_dim * (type == MK_TYPE_FP32 ? 4 : 2);
-  if (NORM) p.tokens = p.rows >= 1024 ? kRopeTokens : 1;
-  else p.tokens = p.rows < 1024 ? 1 : p.rows >= 4096 && row_bytes < 8192 ? kRopeTokens : 2;
+  const int most = NORM ? 2 * 152 * (type == MK_TYPE_FP32 ? 4 : 7) : 4095;  // rows in blocks of two
+  const int64_t narrow = NORM ? 16384 : 8192;
+  p.tokens = p.rows < 1024 ? 1 : p.rows > most && row_bytes < narrow ? kRopeTokens : 2;
   cudaStream_t st = (cudaStream_t)stream;
   if (type == MK_TYPE_FP32) {
     if (cache->head_dim == 64) launch_rope<float, 64, NORM>(p, st);
