@@ -22,6 +22,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;  // that take values; one more warp decides
 constexpr int kMaxCluster = 16;
 constexpr int E = 8;  // a thread takes values by eight
+constexpr float kSlack = 8.f;  // log2 of how far a weight may exceed 1 while a thread adds up
 
 struct VerifyParams {
   const void *logits, *draft;
@@ -227,6 +228,24 @@ __device__ __forceinline__ int warp_first(float x, float top, int at) {
   return __reduce_min_sync(0xffffffffu, x == top ? at : INT_MAX);
 }
 
+// A thread's sum of weights, of groups of them. What an add rounds off goes into the next one: a
+// block that has a row to itself adds up vocab / 2048 groups a thread, which without that could all
+// be rounded the same way (2^-15 of a sum of 2^19 equal values).
+// In units of 2^-24 a row's sum is then off by 46 at most (10 adds of 32 weights, 2 here, 5 for the
+// lane's, the warp's and the block's reference each, 19 adds of lanes and parts, the reciprocal's 4),
+// and what its weights are off by: of a weight 2^-z four for the exponential and 4 ln 2 z for the
+// difference, log2(e) / temperature and their product; the sum's are of z up to log2 vocab, at
+// 2^30 88. A probability e^-28 of the largest: 46 + 88 + 4 + 112 = 250 < 256.
+struct Sum {
+  float total = 0.f, over = 0.f;  // over: what total is too large by
+  __device__ __forceinline__ void add(float x) {
+    const float y = x - over, t = total + y;
+    over = (t - total) - y;
+    total = t;
+  }
+  __device__ __forceinline__ void scale(float f) { total *= f, over *= f; }
+};
+
 // ---- the kernel --------------------------------------------------------------------------
 
 // The rows that a pass goes over, and a group of eight values of each.
@@ -367,22 +386,30 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
     if (step > 0 && p.span > 16 / (int)sizeof(L) * kStride) fetch_part(row, sizeof(L));
     f.only = -1;
     f.top = -INFINITY;
-    float sum = 0.f;
+    Sum all_of;
     int at = INT_MAX;  // heat not above 0: the first index of the largest
     const Rows<L> values{row, -INFINITY};
     if (heat > 0.f) {
+      // (the reference moves only where it has to, by 2^kSlack: what its moves round falls off
+      // with what they scale, however often a row's largest value changes)
       constexpr int U = 8 / sizeof(L);
+      float high = -INFINITY;
       over_values<VEC, U>(first, hi, values, [&](int, const auto& x) {
         float top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < U; ++u) top = fmaxf(top, largest(x[u].v));
-        if (top > f.top) {
-          sum = sum > 0.f ? sum * fast_exp2((f.top - top) * f.k) : 0.f;
+        high = fmaxf(high, top);
+        if ((top - f.top) * f.k > kSlack) {
+          all_of.scale(fast_exp2((f.top - top) * f.k));
           f.top = top;
           f.set_plain();
         }
-        if (f.top > -INFINITY) sum += f.sum_of(x);
+        if (f.top > -INFINITY) all_of.add(f.sum_of(x));
       });
+      if (high > f.top) {
+        all_of.scale(fast_exp2((f.top - high) * f.k));
+        f.top = high;
+      }
     } else {
       over_values<VEC, 1>(first, hi, values, [&](int i, const auto& x) {
 #pragma unroll
@@ -432,6 +459,7 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
     {
       const float top = warp_max(f.top);
       if (heat > 0.f) {
+        float sum = all_of.total;
         sum = warp_sum(f.top == top ? sum : sum > 0.f ? sum * fast_exp2((f.top - top) * f.k) : 0.f);
         exchange(make_uint2(__float_as_uint(top), __float_as_uint(sum)));
       } else {
@@ -499,14 +527,15 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
         c += mass;
         if (j + 1 == kids) break;  // nobody asks for what is left
         if (j == 0) fetch_part(draft, sizeof(Q));
-        float sum = 0.f;
+        Sum sum;
         over_values<VEC, 1>(first, hi, Rows<L, Q>{row, -INFINITY, {draft, 0.f}}, [&](int i, const auto& x) {
           float w[E];
           f.weights(x[0].v, i, w);
 #pragma unroll
-          for (int e = 0; e < E; ++e) sum += fmaxf(w[e] * f.inv - c * probability(x[0].rest.v[e]), 0.f);
+          for (int e = 0; e < E; ++e) w[e] = fmaxf(w[e] * f.inv - c * probability(x[0].rest.v[e]), 0.f);
+          sum.add(((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7])));
         });
-        exchange(make_uint2(__float_as_uint(warp_sum(sum)), 0));
+        exchange(make_uint2(__float_as_uint(warp_sum(sum.total)), 0));
         float all = 0.f;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) all += __uint_as_float(part(i, make_uint2(0, 0)).x);

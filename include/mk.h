@@ -437,9 +437,10 @@ int mk_rope_append(const mk_rope* rope, const mk_cache* cache, int layer, int ba
    their rotation: a head x becomes x w / sqrt(mean of x^2 + eps), in fp32, in the
    same pass; only the rotated value is rounded. q_norm, k_norm: DEVICE bf16
    [head_dim], 16-byte aligned, shared by the heads; NULL: ones. eps 1e-30 to 1. The v
-   rows pass as they are. A NaN or an infinity in a head of q or k stays with that head. The
-   other arguments and the errors are those of mk_rope_append. (mk_decode_step and the
-   other calls with a handle do not normalise heads.) */
+   rows pass as they are. A NaN or an infinity in a head of q or k stays with that head, all
+   of whose values may be NaN then; one among the weights stays with its pair (behind
+   rotary_dim: two neighbours). The other arguments and the errors are those of
+   mk_rope_append. (mk_decode_step and the other calls with a handle do not normalise heads.) */
 int mk_norm_rope_append(const mk_rope* rope, const void* q_norm, const void* k_norm, float eps,
                         const mk_cache* cache, int layer, int batch, int n_tokens, int n_heads,
                         int type, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -535,9 +536,9 @@ int mk_tree_accept_workspace(int batch, int n_tokens, int vocab, size_t* bytes);
    is a sample of r. A token outside [0, vocab) is passed over, and what hangs off it
    with it. Where rounding leaves nothing of r, next is sampled from p. At a row
    without a logit above -inf there is no p: the walk ends there and next is -1.
-   Probabilities and sums are fp32, to 2^-16 of their value at worst (differences: of
-   what is subtracted): a comparison closer than that may fall either way, the same
-   way each time. Outputs as mk_tree_accept's path, accepted and next. No workspace.
+   Probabilities and sums are fp32, at any vocab to 2^-16 of their value for logits up to 28
+   temperatures below the row's largest (others to 2^-15; differences: of what is
+   subtracted): a comparison closer than that may fall either way, the same way each time. Outputs as mk_tree_accept's path, accepted and next. No workspace.
    Errors: MK_ERR_INVALID, MK_ERR_CUDA. */
 int mk_tree_verify(int batch, int n_tokens, int vocab, int type, const void* logits,
                    int64_t logits_stride, int draft_type, const void* draft, int64_t draft_stride,

@@ -339,3 +339,39 @@ def test_binding_refusals():
             f()
         assert e.value.code == mk.MK_ERR_INVALID, i
     torch.cuda.synchronize()
+
+
+@gpu
+def test_long_sums_of_a_residual():
+    """A block that has a whole row to itself (153 sequences) adds up 2048 equal values a thread, each of which serial
+    sums in fp32 would round the same way (2^-15 of the sum in all). Thresholds 2^-16 on either side of the exact one
+    fall on theirs: a sum loses 2^-18.5 here (adds of a tree of 32 or 8, of a warp, of its parts, each compensated or 2^-24)."""
+    B, V = 153, 2**19
+    logits = torch.zeros((B, 3, V), dtype=BF16, device="cuda")  # p = 2^-19, exactly
+    draft = torch.full((B, 3, V), 2.0**-19 * (0.5 - 2.0**-15), device="cuda")  # r = 2^-20 (1 + 2^-14) of each
+    tokens = torch.tensor([0, 5, 9], dtype=torch.int32, device="cuda").expand(B, 3).contiguous()
+    draft[:, 0, 5], draft[:, 0, 9] = 0.5, 0.8 * 2.0**-19
+    q, p = float(draft[0, 0, 9]), 2.0**-19
+    left = (V - 2) * 2.0**-20 * (1 + 2.0**-14) + (p - q)
+    limit = (p - q) / (q * left)  # child 9 is accepted below it
+    uniform = torch.full((B, 3), 0.9, device="cuda")
+    uniform[0::2, 2], uniform[1::2, 2] = limit * (1 - 2.0**-16), limit * (1 + 2.0**-16)
+    path, accepted, last = mk.tree_verify(logits, tokens, uniform, torch.ones((B, V), device="cuda"),
+                                          torch.tensor([-1, 0, 0], dtype=torch.int32, device="cuda").expand(B, 3).contiguous(), draft=draft)
+    assert (accepted[0::2] == 2).all() and (path[0::2, 1] == 2).all() and (accepted[1::2] == 1).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [FP32, BF16])
+def test_long_sums_of_ascending_logits(dtype):
+    """Each value of a thread is its largest so far: its sum is not taken to a new reference, rounded, each time."""
+    B, V = 153, 2**22
+    row = torch.arange(V, device="cuda") * 2.0**-37 if dtype == FP32 else torch.arange(V, device="cuda") // 16384 * 2.0**-15
+    row = row.to(dtype)
+    logits = row.expand(B, 2, V).contiguous()
+    tokens = torch.tensor([0, V // 2], dtype=torch.int32, device="cuda").expand(B, 2).contiguous()
+    limit = torch.softmax(row.double(), -1)[V // 2].item()
+    uniform = torch.zeros((B, 2), device="cuda")
+    uniform[0::2, 1], uniform[1::2, 1] = limit * (1 - 2.0**-16), limit * (1 + 2.0**-16)
+    path, accepted, last = mk.tree_verify(logits, tokens, uniform, torch.ones((B, V), device="cuda"))
+    assert (accepted[0::2] == 2).all() and (accepted[1::2] == 1).all()
