@@ -572,7 +572,7 @@ def _ints(t, device, what: str, shape):
     """The pointer of an int32 index tensor (contiguous, on `device`)."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+    if getattr(t, "dtype", None) != torch.int32 or t.device != device or not t.is_contiguous():
         raise _bad(f"{what} must be a contiguous int32 tensor on {device}")
     if t.shape != shape:
         raise _bad(f"{what} has the shape {tuple(t.shape)}, not {shape}")
@@ -580,7 +580,7 @@ def _ints(t, device, what: str, shape):
 
 
 def _type_of(t, what: str) -> int:
-    kind = _TYPES.get(t.dtype)
+    kind = _TYPES.get(getattr(t, "dtype", None))
     if kind is None:
         raise _bad(f"{what} must be bfloat16 or float32")
     return kind
@@ -588,7 +588,7 @@ def _type_of(t, what: str) -> int:
 
 def _queries(q, cache) -> tuple:
     """(shape, type, row stride) of q [B][T][nh][D]."""
-    shape = q.shape
+    shape = getattr(q, "shape", ())
     if len(shape) != 4 or shape[3] != cache.head_dim:
         raise _bad("q must be [batch][tokens][heads][head_dim], the cache's head_dim")
     return shape, _type_of(q, "q"), _heads(q, shape, q.dtype, cache.device, "q")
@@ -596,9 +596,9 @@ def _queries(q, cache) -> tuple:
 
 def _heads(t, shape, dtype, device, what: str) -> int:
     """The row stride of t [B][T][heads][D]: heads packed, rows evenly spaced."""
-    if t.dtype != dtype or t.device != device or t.shape != shape:
-        raise _bad(f"{what} must be a {dtype} tensor of the shape {tuple(shape)} on {device}, not "
-                   f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if getattr(t, "dtype", None) != dtype or t.device != device or t.shape != shape:
+        has = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else repr(t)
+        raise _bad(f"{what} must be a {dtype} tensor of the shape {tuple(shape)} on {device}, not {has}")
     b, n, h, d = shape
     sb, sn, sh, sd = t.stride()
     if sd != 1 or (h > 1 and sh != d):
@@ -648,7 +648,7 @@ def rope_append(rope: Rope, cache: Cache, layer: int, q, k, v, starts, parents=N
 def _norm_weights(t, cache: Cache, what: str):
     if t is None:
         return None
-    if t.dtype != torch.bfloat16 or t.device != cache.device or not t.is_contiguous():
+    if getattr(t, "dtype", None) != torch.bfloat16 or t.device != cache.device or not t.is_contiguous():
         raise _bad(f"{what} must be a contiguous bfloat16 tensor on {cache.device}")
     if t.shape != (cache.head_dim,):
         raise _bad(f"{what} has the shape {tuple(t.shape)}, not {(cache.head_dim,)}")
@@ -712,8 +712,8 @@ def prefix_attention(cache: Cache, layer: int, q, first, prefix, starts, parents
             return prefix_attention(cache, layer, q, first, prefix, starts, parents, counts, scale, out)
     shape, kind, qs = _queries(q, cache)
     b, n, nh, d = shape
-    if len(first.shape) != 1:
-        raise _bad("first must be [groups]")
+    if len(getattr(first, "shape", ())) != 1:
+        raise _bad("first must be a tensor [groups]")
     groups = first.shape[0]
     fp, xp = _ints(first, dev, "first", (groups,)), _ints(prefix, dev, "prefix", (groups,))
     sp = _ints(starts, dev, "starts", (b,))
@@ -736,6 +736,13 @@ def prefix_attention(cache: Cache, layer: int, q, first, prefix, starts, parents
     return out
 
 
+def _logits(t) -> tuple:
+    """(device, shape) of logits [B][T][V]."""
+    if not getattr(t, "is_cuda", False) or len(t.shape) != 3:
+        raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
+    return t.device, t.shape
+
+
 def _rows(t, shape, what: str) -> int:
     """The row stride of t [B][T][V]: rows packed and evenly spaced."""
     b, n, vocab = shape
@@ -749,9 +756,7 @@ def tree_accept(logits, tokens, parents=None, counts=None, stream=None):
     """mk_tree_accept: logits [B][T][V] (bf16 or fp32), tokens [B][T] int32.
     Returns int32 (choices [B][T], path [B][T], accepted [B], next [B])."""
     _use_torch()
-    dev, shape = logits.device, logits.shape
-    if not logits.is_cuda or len(shape) != 3:
-        raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
+    dev, shape = _logits(logits)
     if (other := _elsewhere(dev, stream)) is not None:
         with other:
             return tree_accept(logits, tokens, parents, counts)
@@ -795,9 +800,7 @@ def tree_verify(logits, tokens, uniform, noise, parents=None, counts=None, draft
     were sampled from, or None; temperature [B] fp32. Returns int32 (path [B][T],
     accepted [B], next [B])."""
     _use_torch()
-    dev, shape = logits.device, logits.shape
-    if not logits.is_cuda or len(shape) != 3:
-        raise _bad("logits must be a CUDA tensor [batch][tokens][vocab]")
+    dev, shape = _logits(logits)
     if (other := _elsewhere(dev, stream)) is not None:
         with other:
             return tree_verify(logits, tokens, uniform, noise, parents, counts, draft, temperature)
@@ -806,11 +809,11 @@ def tree_verify(logits, tokens, uniform, noise, parents=None, counts=None, draft
     stride = _rows(logits, shape, "logits")
     draft_kind, draft_at, draft_stride = 0, None, 0
     if draft is not None:
-        if draft.device != dev or draft.shape != shape:
+        if getattr(draft, "device", None) != dev or draft.shape != shape:
             raise _bad(f"draft must be a tensor of the shape {tuple(shape)} on {dev}")
         draft_kind, draft_stride = _type_of(draft, "draft"), _rows(draft, shape, "draft")
         draft_at = draft.data_ptr()
-    if noise.dtype != torch.float32 or noise.device != dev or noise.shape != (b, vocab) or (
+    if getattr(noise, "dtype", None) != torch.float32 or noise.device != dev or noise.shape != (b, vocab) or (
             vocab > 1 and noise.stride(1) != 1):
         raise _bad(f"noise must be a float32 tensor of the shape {(b, vocab)} on {dev}, its rows packed")
     tp, up = _ints(tokens, dev, "tokens", (b, n)), _floats(uniform, dev, "uniform", (b, n))
@@ -835,7 +838,7 @@ def cache_compact(cache: Cache, starts, path, accepted, stream=None):
     if (other := _elsewhere(dev, stream)) is not None:
         with other:
             return cache_compact(cache, starts, path, accepted)
-    if len(path.shape) != 2:
+    if len(getattr(path, "shape", ())) != 2:
         raise _bad("path must be [batch][tokens]")
     b, n = path.shape
     sp = _ints(starts, dev, "starts", (b,))
