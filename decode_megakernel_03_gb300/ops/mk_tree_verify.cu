@@ -232,10 +232,10 @@ __device__ __forceinline__ int warp_first(float x, float top, int at) {
 // block that has a row to itself adds up vocab / 2048 groups a thread, which without that could all
 // be rounded the same way (2^-15 of a sum of 2^19 equal values).
 // In units of 2^-24 a row's sum is then off by 46 at most (10 adds of 32 weights, 2 here, 5 for the
-// lane's, the warp's and the block's reference each, 19 adds of lanes and parts, the reciprocal's 4),
-// and what its weights are off by: of a weight 2^-z four for the exponential and 4 ln 2 z for the
-// difference, log2(e) / temperature and their product; the sum's are of z up to log2 vocab, at
-// 2^30 88. A probability e^-28 of the largest: 46 + 88 + 4 + 112 = 250 < 256.
+// lane's, the warp's and the block's reference each, 14 adds of lanes and parts, the reciprocal and
+// its product 5), and by what its weights are off by: of a weight 2^-z four for the exponential and
+// 4 ln 2 z for the difference, log2(e) / temperature and their product; z up to log2 vocab matters,
+// at 2^30 88. A probability e^-28 of the largest: 46 + 88 + 4 + 112 = 250 < 256.
 struct Sum {
   float total = 0.f, over = 0.f;  // over: what total is too large by
   __device__ __forceinline__ void add(float x) {
@@ -625,47 +625,58 @@ __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_c
   }
 }
 
-// Blocks of a cluster: the largest power of two that leaves every block of the call resident
-// at once, two to an SM, and gives each thread of it eight values.
-int cluster_of(int batch, int vocab, int n_sm) {
-  int c = kMaxCluster;
-  while (c > 1 && (batch * c > 2 * n_sm || vocab < c * kThreads * E)) c /= 2;
-  return c;
-}
-
+// Launches with clusters of the largest power of two that gives each thread of a block eight values
+// and leaves every cluster of the call resident at once, as the device says for this kernel: a
+// cluster lies in one GPC, so that 14 or 15 of 16 blocks (by the chip), 36 of 8 and 74 of 4 are
+// resident where two blocks to each of 152 SMs would be 19, 38 and 76. One more than fit would wait
+// for a whole walk: chains of 4 over 128256 values, 16 sequences with clusters of 16 29.6 us, of 8
+// 18.8; 38 with 8 40.9, with 4 32.8; 76 with 4 59.7, with 2 52.6.
 template <typename L, typename Q, bool VEC>
-int launch(const VerifyParams& p, int batch, int blocks, cudaStream_t st) {
+int launch(VerifyParams p, int batch, cudaStream_t st) {
+  constexpr int kSizes = 4, kDevices = 64;  // of 16, 8, 4 and 2 blocks
+  static std::atomic<int> resident[kDevices][kSizes];  // 1 + how many; 0: not asked yet
   auto* fn = verify_kernel<L, Q, VEC>;
-  static std::atomic<uint64_t> ready{0};
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return op_cuda(e, "mk_tree_verify");
-  const uint64_t bit = 1ull << (device & 63);
-  if (device >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return op_cuda(e, "mk_tree_verify");
-    ready.fetch_or(bit, std::memory_order_release);
-  }
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = blocks;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  attr.val.clusterDim.x = attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)batch * blocks);
   cfg.blockDim = dim3(kThreads + 32);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  int blocks = 1;
+  for (int i = 0; i < kSizes && blocks == 1; ++i) {
+    const int size = kMaxCluster >> i;
+    if (p.V < size * kThreads * E) continue;
+    int fit = device < kDevices ? resident[device][i].load(std::memory_order_acquire) : 0;
+    if (fit == 0) {
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return op_cuda(e, "mk_tree_verify");
+      attr.val.clusterDim.x = size;
+      cfg.gridDim = dim3(size);
+      e = cudaOccupancyMaxActiveClusters(&fit, fn, &cfg);
+      if (e != cudaSuccess) return op_cuda(e, "mk_tree_verify");
+      ++fit;
+      if (device < kDevices) resident[device][i].store(fit, std::memory_order_release);
+    }
+    if (batch < fit) blocks = size;
+  }
+  p.span = (int)(((int64_t)p.V + blocks - 1) / blocks + E - 1) / E * E;
+  attr.val.clusterDim.x = blocks;
+  cfg.gridDim = dim3((unsigned)batch * blocks);
   return op_cuda(cudaLaunchKernelEx(&cfg, fn, p), "mk_tree_verify");
 }
 
 template <bool VEC>
-int launch_types(const VerifyParams& p, int type, bool narrow, int batch, int blocks, cudaStream_t st) {
+int launch_types(const VerifyParams& p, int type, bool narrow, int batch, cudaStream_t st) {
   if (type == MK_TYPE_FP32)
-    return narrow ? launch<float, uint16_t, VEC>(p, batch, blocks, st)
-                  : launch<float, float, VEC>(p, batch, blocks, st);
-  return narrow ? launch<uint16_t, uint16_t, VEC>(p, batch, blocks, st)
-                : launch<uint16_t, float, VEC>(p, batch, blocks, st);
+    return narrow ? launch<float, uint16_t, VEC>(p, batch, st)
+                  : launch<float, float, VEC>(p, batch, st);
+  return narrow ? launch<uint16_t, uint16_t, VEC>(p, batch, st)
+                : launch<uint16_t, float, VEC>(p, batch, st);
 }
 
 }  // namespace
@@ -700,14 +711,8 @@ extern "C" int mk_tree_verify(int batch, int n_tokens, int vocab, int type, cons
       !aligned(temperature, 4))
     return op_fail(MK_ERR_INVALID,
                    "noise: a stride of at least vocab; noise, uniform, temperature: aligned to 4 bytes");
-  int device = 0, n_sm = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, device);
-  if (e != cudaSuccess) return op_cuda(e, "mk_tree_verify");
-  const int blocks = cluster_of(batch, vocab, n_sm);
-  const int span = (int)(((int64_t)vocab + blocks - 1) / blocks + E - 1) / E * E;
   const VerifyParams p{logits, draft, logits_stride, draft_stride, noise_stride, temperature, uniform,
-                       noise, tokens, parents, counts, path, accepted, next, n_tokens, vocab, span};
+                       noise, tokens, parents, counts, path, accepted, next, n_tokens, vocab, 0};
   cudaStream_t st = (cudaStream_t)stream;
   const bool narrow = draft && draft_type == MK_TYPE_BF16;
   auto by16 = [](const void* at, int64_t stride, size_t size) {
@@ -715,6 +720,6 @@ extern "C" int mk_tree_verify(int batch, int n_tokens, int vocab, int type, cons
   };
   const bool vec = by16(logits, logits_stride, size) && by16(noise, noise_stride, 4) &&
                    (!draft || by16(draft, draft_stride, draft_size));
-  return vec ? launch_types<true>(p, type, narrow, batch, blocks, st)
-             : launch_types<false>(p, type, narrow, batch, blocks, st);
+  return vec ? launch_types<true>(p, type, narrow, batch, st)
+             : launch_types<false>(p, type, narrow, batch, st);
 }

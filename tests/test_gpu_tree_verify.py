@@ -375,3 +375,18 @@ def test_long_sums_of_ascending_logits(dtype):
     uniform[0::2, 1], uniform[1::2, 1] = limit * (1 - 2.0**-16), limit * (1 + 2.0**-16)
     path, accepted, last = mk.tree_verify(logits, tokens, uniform, torch.ones((B, V), device="cuda"))
     assert (accepted[0::2] == 2).all() and (accepted[1::2] == 1).all()
+
+
+@gpu
+@pytest.mark.parametrize("V", [33000, 9000])
+def test_any_number_of_sequences(V):
+    """A sequence's outcome does not depend on how many there are, and with them on the blocks that each has."""
+    a = make(100, 3, 6, V, BF16, FP32, "tree")
+    want = expected(a)
+    assert want[3].min() > CLEAR
+    d = on_device(a)
+    for B in (1, 2, 13, 14, 15, 16, 19, 20, 36, 37, 38, 39, 73, 74, 75, 76, 77, 152, 153, 305):
+        at = torch.arange(B, device="cuda") % 3
+        got = call({n: None if x is None else x[at].contiguous() for n, x in d.items()})
+        for g, w in zip(got, want):
+            assert np.array_equal(g.cpu().numpy(), w[at.cpu().numpy()]), B
