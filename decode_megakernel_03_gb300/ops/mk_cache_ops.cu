@@ -138,7 +138,7 @@ struct RopeRows {
   int pos[kRopeTokens];
   uint32_t row[kRopeTokens];
 };
-template <int D>
+template <int D, int THREADS>
 __device__ __forceinline__ void find_rows(const RopeParams& p, RopeRows<D>& s) {
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int row0 = blockIdx.x * p.tokens;
@@ -174,7 +174,7 @@ __device__ __forceinline__ void find_rows(const RopeParams& p, RopeRows<D>& s) {
     }
   }
   __syncthreads();
-  for (int i = tid; i < p.tokens * (D / 2); i += blockDim.x) {
+  for (int i = tid; i < p.tokens * (D / 2); i += THREADS) {
     const int tok = i / (D / 2), pair = i % (D / 2);
     float2 v = make_float2(1.f, 0.f);  // behind rotary_dim: passes through
     if (2 * pair < p.rope.rotary_dim) {
@@ -204,17 +204,18 @@ __device__ __forceinline__ void find_rows(const RopeParams& p, RopeRows<D>& s) {
 // 120 us as halves, 6.7 TB/s; U heads of a lane are in flight: 133 us with 2,
 // 136 with 8 (neighbours, four rows in 256 threads, where 4 took 125). 200 rows take 4 to 5 us, a
 // launch's latency; a block of a single row has 256 threads there, with 128 it took 0.2 us more.
-template <typename T, int D, int PIECE>
-__global__ void __launch_bounds__(kRopeRowThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+template <typename T, int D, int PIECE, int THREADS>
+__global__ void __launch_bounds__(THREADS) rope_append_kernel(const __grid_constant__ RopeParams p) {
   constexpr int LPH = D / 8, HPW = 32 / LPH, U = 4;
   __shared__ RopeRows<D> s;
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int WARPS = THREADS / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row0 = blockIdx.x * p.tokens;
-  find_rows<D>(p, s);
+  find_rows<D, THREADS>(p, s);
 
-  const int tok = warp % p.tokens;  // tokens divides warps
+  const int tok = warp % p.tokens;  // tokens divides WARPS
   if (s.pos[tok] < 0) return;
-  const int n_kv = p.cache.n_kv, heads = p.nh + 2 * n_kv, step = warps / p.tokens * HPW;
+  const int n_kv = p.cache.n_kv, heads = p.nh + 2 * n_kv, step = WARPS / p.tokens * HPW;
   const int c = lane % LPH, half = p.rope.rotary_dim / 2;
   const int64_t row = row0 + tok;
   const uint32_t crow = s.row[tok];
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 7 : 4) norm_rop
   // every row is there
   const bool early = p.counts == nullptr && row < p.rows;
   if (early) fetch_queries(first);
-  find_rows<D>(p, s);
+  find_rows<D, kRopeThreads>(p, s);
   if (s.pos[tok] < 0) return;
   const uint32_t crow = s.row[tok];
 
@@ -442,7 +443,8 @@ template <typename T, int D, int PIECE, bool NORM>
 void launch_rope(const RopeParams& p, cudaStream_t st) {
   const dim3 grid((p.rows + p.tokens - 1) / p.tokens);
   if constexpr (NORM) norm_rope_append_kernel<T, D, PIECE><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_append_kernel<T, D, PIECE><<<grid, p.tokens == 1 ? kRopeRowThreads : kRopeThreads, 0, st>>>(p);
+  else if (p.tokens == 1) rope_append_kernel<T, D, PIECE, kRopeRowThreads><<<grid, kRopeRowThreads, 0, st>>>(p);
+  else rope_append_kernel<T, D, PIECE, kRopeThreads><<<grid, kRopeThreads, 0, st>>>(p);
 }
 template <typename T, int D, bool NORM>
 void launch_rope(const RopeParams& p, cudaStream_t st) {
