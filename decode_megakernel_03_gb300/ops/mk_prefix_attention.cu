@@ -14,7 +14,7 @@
 // writes its rows.
 //
 // Measured on the 8B shape, bf16: 64 samples of two documents (32768 and 26215 keys, 256
-// to 2048 own keys, 4 nodes each; 531 MB, 123 GFLOP) 211 us: the prefixes' tiles are
+// to 2048 own keys, 4 nodes each; 531 MB, 123 GFLOP) 222 us (211 without the code of kRun): the prefixes' tiles are
 // bound by the products, which both parts of the weights go through (4400 cycles for two
 // blocks of rows, 3072 of them products), the own keys' by the beginnings and ends of 512
 // items (9000 cycles each) and their tiles (2000). 32 samples behind 8192 keys, 16 to 512
@@ -575,10 +575,9 @@ int mk_prefix_attention(const mk_cache* cache, int layer, int batch, int n_token
   p.starts = starts, p.parents = parents, p.counts = counts;
   p.B = batch, p.T = n_tokens, p.nh = n_heads, p.G = n_heads / cache->n_kv_heads;
   p.tile_log2 = 7;
-  // What an item's beginning and end are worth, in tiles (32 samples behind
-  // 8192 keys, bf16, one block of rows: 2, 3, 4, 5 41.2, 39.3, 41.0, 43.3 us; 64 samples of two prompts
-  // of up to 32768 keys, two blocks: 4, 5, 6, 7 227, 223, 215, 217; 24 samples in fp32: 2, 3, 4 55.2,
-  // 57.8, 59.7)
+  // What an item's beginning and end are worth, in tiles (32 samples behind 8192 keys, bf16, one
+  // block of rows: 2, 3, 4, 5 39.3, 37.4, 38.4, 40.6 us; 64 samples of two prompts of up to 32768
+  // keys, two blocks: 4, 5, 6, 7, 8 236, 224, 221, 223, 225; 24 samples in fp32: 2, 3, 4 50.8, 53.7, 55.6)
   p.extra = type == MK_TYPE_FP32 ? 2 : pl.row_tile > 128 ? 6 : 3;
   p.row_tile = pl.row_tile, p.row_tiles = 1,
   p.row_log2 = pl.row_tile == 32 ? 5 : pl.row_tile == 128 ? 7 : 8, p.groups = pl.groups;

@@ -313,7 +313,7 @@ __device__ __forceinline__ void over_values(int first, int hi, const R& rows, Ta
 // chains of 8, 132 MB of rows, take 52 us, 2.5 TB/s. Measured and slower: copies to shared
 // memory ahead of the sums, 16 bytes a thread each (4300 cycles for the 1900); two groups of
 // values at a time in the race or the residual's sum (registers; 59 us); 512 threads a block
-// (clusters of 16 that no longer fit all at once, it seems: 46 us for 8 sampled trees instead of 35).
+// (clusters of 16 of which fewer are resident: 46 us for 8 sampled trees instead of 35).
 template <typename L, typename Q, bool VEC>
 __global__ void __launch_bounds__(kThreads + 32, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ Shared sm;

@@ -475,7 +475,8 @@ int mk_tree_attention_workspace(const mk_cache* cache, int batch, int n_tokens, 
                                 int type, size_t* bytes);
 
 /* mk_tree_attention for a batch whose groups share a prefix (the samples of a prompt,
-   mk_pages_fork): the prefix's keys are read once for all sequences of a group.
+   mk_pages_fork): the prefix's keys are read once for up to 128 or 256 rows (query heads of
+   a kv-head, nodes, sequences) of a group, in fp32 for 32 where the mean group has no more.
    first, prefix: DEVICE int32 [n_groups], n_groups 1 to batch. Group i is the
    sequences from first[i] on, up to the next group's first (the last: to the batch's
    end). A first below the one before it or outside [0, batch] is taken at the nearest
