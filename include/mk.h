@@ -455,7 +455,8 @@ int mk_norm_rope_append(const mk_rope* rope, const void* q_norm, const void* k_n
    heads per kv-head; n_tokens 1 to MK_MAX_TREE. Softmax of scale * (q . k) in
    fp32; its weights enter the product with the values as bf16 parts that hold them
    to 2^-16 (fp32 calls: weights and queries to 2^-24); a bf16 call's sums lose at most 2^-13
-   of themselves, however long the context, as the matrix unit truncates. A row that sees no key is 0;
+   of themselves, however long the context, as the matrix unit truncates. A row that sees
+   no key is 0;
    NaN and infinities in rows it does not see do not reach it. Infinities that it does
    see in keys or in the context's values may make it NaN where the formula gives
    an infinity or a weight of 0. out may be q (with q's stride). Deterministic: the same
@@ -539,7 +540,8 @@ int mk_tree_accept_workspace(int batch, int n_tokens, int vocab, size_t* bytes);
    without a logit above -inf there is no p: the walk ends there and next is -1.
    Probabilities and sums are fp32, at any vocab to 2^-16 of their value for logits up to 28
    temperatures below the row's largest (others to 2^-15; differences: of what is
-   subtracted): a comparison closer than that may fall either way, the same way each time. Outputs as mk_tree_accept's path, accepted and next. No workspace.
+   subtracted): a comparison closer than that may fall either way, the same way each
+   time. Outputs as mk_tree_accept's path, accepted and next. No workspace.
    Errors: MK_ERR_INVALID, MK_ERR_CUDA. */
 int mk_tree_verify(int batch, int n_tokens, int vocab, int type, const void* logits,
                    int64_t logits_stride, int draft_type, const void* draft, int64_t draft_stride,
